@@ -308,13 +308,135 @@ THRIFT_API thrift_status thrift_decode_step(const thrift_decode_shape *shape, co
                                             const void *v, const thrift_decode_cache *cache, void *o,
                                             float *lse, void *ws, size_t ws_bytes, void *stream);
 
+/* ------------------------------------------------------------------------
+ * The paged 8-bit KV cache: append, attention, eviction.
+ *
+ * HyQuant: Hybrid-Precision Quantization for LLM Attention (abstract) serves
+ * decoding from a compressed cache and singles out sink tokens, the local
+ * window and the tokens that many queries attend to.  These calls are this
+ * library's serving form of it: sequences of different lengths share one pool
+ * of pages; a page holds `page` tokens of every kv head as e4m3 codes with one
+ * power-of-two scale 2^e per page, head and operand (K, V), so a value is
+ * code * 2^e.  Sequence b's token t is slot t % page of pool page
+ * table[b * table_cols + t / page]; lens[b] is its number of tokens, the new
+ * ones of the current call included.
+ *
+ * New tokens are packed: sequence b's are rows [cu[b], cu[b + 1]) and stand at
+ * positions lens[b] - (cu[b + 1] - cu[b]) and up; rows outside every such range
+ * are neither read nor written.  cu NULL means one token per sequence (n == B).
+ *
+ * table, lens and cu are device arrays that the kernels read when they run, so
+ * a captured call may be replayed with other contents; max_q (new tokens of a
+ * sequence), max_len (tokens of a sequence) and n bound them on the host.  The
+ * kernels check them: a length outside [0, min(max_len, table_cols * page)]
+ * (its sequence then counts as empty), a range of new tokens outside [0, n] or
+ * longer than max_q (counts as none), a page number outside the pool on a page
+ * that has visible tokens (they count as not visible; append writes nothing,
+ * evict zeros) set bit 16 of the device error word, which
+ * thrift_device_status reports as THRIFT_ERR_INVALID.  Table entries of pages
+ * that a call need not touch are not read as page numbers and may hold anything
+ * (pages that a window has left behind can be freed).  Slots past a sequence's
+ * end may hold anything, NaN codes included.
+ *
+ * Limits: d in {64, 128}; page in {16, 32, 64, 128}; B * Hkv <= 65535;
+ * table_cols * page <= 2^24 tokens a sequence; num_pages <= 2^30; n * Hq < 2^31.
+ * Pool pointers 16-byte aligned, w 16, table, lens, cu, lse 4.
+ * ------------------------------------------------------------------------ */
+enum { THRIFT_BF16 = 0, THRIFT_FP16 = 1 };
+
+typedef struct {
+  int32_t B, Hq, Hkv, d;  /* Hq: query heads (append and evict ignore it); Hq % Hkv == 0 */
+  int32_t page;           /* tokens per page */
+  int32_t table_cols;     /* entries of a sequence's row of `table` */
+  int32_t n, max_q;       /* packed rows of new tokens; bound on one sequence's */
+  int32_t max_len;        /* bound on lens[b], 1 <= max_len <= table_cols * page */
+  int32_t dtype;          /* of q, k, v, o: THRIFT_BF16 or THRIFT_FP16 */
+} thrift_kv8_shape;
+
+typedef struct {
+  uint8_t *k, *v;    /* [num_pages][Hkv][page][d] e4m3 codes */
+  uint8_t *ks, *vs;  /* [num_pages][Hkv] e + 127 */
+  int32_t num_pages;
+} thrift_kv8_cache;
+
+/* Bytes of one field of a pool of num_pages pages: 0 k, 1 v, 2 ks, 3 vs (0 for a bad argument). */
+THRIFT_API size_t thrift_kv8_cache_bytes(int32_t num_pages, int32_t Hkv, int32_t page, int32_t d, int field);
+
+/*
+ * Quantise new tokens into their sequences' pages.  k, v: [n][Hkv][d] rows of
+ * shape->dtype whose token strides are k_stride and v_stride elements
+ * (multiples of 8, >= Hkv * d).  A page's e is the smallest integer >= -127
+ * with amax <= 448 * 2^e over its new tokens; if the page already held tokens
+ * of the sequence, the larger of that and its old e, and when e grows the old
+ * codes are rounded again to the nearest code of value * 2^-e (exact but for
+ * e4m3 subnormals).  Codes round to nearest, ties to even.  Pages that two
+ * sequences share must be full: one being appended to is written by one
+ * sequence only.  Inputs must be finite.
+ */
+THRIFT_API thrift_status thrift_kv8_append(const thrift_kv8_shape *shape, const thrift_kv8_cache *cache,
+                                           const void *k, int64_t k_stride, const void *v, int64_t v_stride,
+                                           const int32_t *table, const int32_t *lens, const int32_t *cu,
+                                           void *stream);
+
+/*
+ * Attention of the new tokens' queries over the cache (which already holds
+ * the new tokens): the query at position p sees tokens t <= p; with window > 0
+ * only those with t > p - window or t < sinks.  q: [n][Hq][d], token stride
+ * q_stride elements (a multiple of 8, >= Hq * d); o: [n][Hq][d] dense; lse:
+ * [n][Hq] FP32 natural-log log-sum-exp or NULL.  A row that sees nothing gets
+ * o = 0, lse = -inf.  Query head h reads kv head h / (Hq / Hkv).
+ * w: NULL, or [B][Hkv][w_cols] FP32 running sums (w_cols >= max_len), to which
+ * the call adds, for every visible token, the attention weights that the
+ * group's query rows gave it: w[b][h][t] += sum exp(s - lse), in a fixed order.
+ * Logits, softmax statistics and sums are FP32; q enters the products as FP16
+ * after an exact power-of-two scaling per row, the probabilities as FP16 (11
+ * bits; scaled so that those above 2^-25 of the largest are normal numbers).
+ * ws: thrift_kv8_attn_workspace_bytes bytes (16-byte aligned; NULL if 0).  Calls
+ * whose work can overlap on the GPU need their own.
+ */
+typedef struct {
+  int32_t window, sinks;  /* window 0: none (sinks is then without effect) */
+  float softmax_scale;    /* 0 selects 1/sqrt(d) */
+} thrift_kv8_mask;
+
+THRIFT_API size_t thrift_kv8_attn_workspace_bytes(const thrift_kv8_shape *shape, const thrift_kv8_mask *mask,
+                                                  int with_w);
+THRIFT_API thrift_status thrift_kv8_attn(const thrift_kv8_shape *shape, const thrift_kv8_mask *mask,
+                                         const thrift_kv8_cache *cache, const void *q, int64_t q_stride,
+                                         const int32_t *table, const int32_t *lens, const int32_t *cu, void *o,
+                                         float *lse, float *w, int64_t w_cols, void *ws, size_t ws_bytes,
+                                         void *stream);
+
+/*
+ * Keep min(lens[b], keep) tokens of every sequence and kv head: the first
+ * `sinks`, the last `recent` (sinks + recent <= keep), and those with the
+ * largest w, the lower position first among equals; each kv head keeps its
+ * own.  They are copied in their order to the pages dst_table of `dst` (may
+ * be the same pool; the pages written must be none that the call reads, nor
+ * written twice); a destination page's e is the largest of its tokens' source
+ * pages', codes rounded again as by append; slots past the last kept token are
+ * left as they were.  dst_lens [B] gets the lengths, dst_w [B][Hkv][dst_w_cols]
+ * the kept tokens' w followed by zeros (it must not overlap w), kept
+ * [B][Hkv][keep] their old positions followed by -1.  Positions are renumbered:
+ * a later window counts kept tokens.  w must not hold NaN; w_cols >= max_len,
+ * dst_cols * page >= min(keep, max_len) <= dst_w_cols.
+ */
+THRIFT_API thrift_status thrift_kv8_evict(const thrift_kv8_shape *shape, const thrift_kv8_cache *cache,
+                                          const int32_t *table, const int32_t *lens, const float *w,
+                                          int64_t w_cols, int32_t keep, int32_t sinks, int32_t recent,
+                                          const thrift_kv8_cache *dst, const int32_t *dst_table, int32_t dst_cols,
+                                          int32_t *dst_lens, float *dst_w, int64_t dst_w_cols, int32_t *kept,
+                                          void *stream);
+
 /*
  * Synchronises `stream`, then reads and clears the library's device error
  * words.  Returns THRIFT_ERR_TIMEOUT if a kernel's bounded wait gave up since
  * the last call (the kernel then returned early and its outputs are
- * undefined); *detail (if non-NULL) receives the raw error word: bits 0-2
+ * undefined), else THRIFT_ERR_INVALID if a kv8 kernel met a bad length, range
+ * or page number (bit 16); *detail (if non-NULL) receives the raw error word: bits 0-2
  * from thrift_attn_fwd (1 producer, 2 tensor-core issuer, 4 softmax), bit 8
- * from thrift_decode_step (a CTA's wait for its bulk-copied cache codes); the
+ * from thrift_decode_step (a CTA's wait for its bulk-copied cache codes), bit
+ * 16 from the kv8 calls' checks, bit 17 from thrift_kv8_attn's waits; the
  * other kernels wait on nothing and set no bit.
  */
 THRIFT_API thrift_status thrift_device_status(void *stream, uint32_t *detail);

@@ -12,6 +12,7 @@ The Python layer only marshals arguments into the C ABI of libthrift.so
 from ._lib import (FORMATS, OP_ATTN, OP_QUANTIZE, OP_QUANTIZE_MX, OP_SELECT, OP_SELECT_VERTICAL, QUANT_FIELDS, Quantized,  # noqa: F401
                    ThriftError, alloc_quantized, attention, attn_fwd, debug_withhold_v_load, decode_quantize_cache,
                    decode_step, device_status,
+                   Kv8Cache, kv8_alloc, kv8_append, kv8_attention, kv8_attention_workspace, kv8_evict,
                    launch_count, lib, make_shape, probe_mma, quant_bytes, quantize, select, shape_of,
                    status_string, version, workspace_bytes)
 from . import workloads  # noqa: F401

@@ -54,6 +54,20 @@ class DecodeCacheStruct(ctypes.Structure):
     _fields_ = [(f, ctypes.c_void_p) for f in DECODE_FIELDS]
 
 
+class Kv8Shape(ctypes.Structure):
+    _fields_ = [(f, ctypes.c_int32) for f in ("B", "Hq", "Hkv", "d", "page", "table_cols", "n", "max_q", "max_len",
+                                              "dtype")]
+
+
+class Kv8CacheStruct(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("ks", ctypes.c_void_p), ("vs", ctypes.c_void_p),
+                ("num_pages", ctypes.c_int32)]
+
+
+class Kv8Mask(ctypes.Structure):
+    _fields_ = [("window", ctypes.c_int32), ("sinks", ctypes.c_int32), ("softmax_scale", ctypes.c_float)]
+
+
 _lib: Optional[ctypes.CDLL] = None
 
 
@@ -100,6 +114,18 @@ def lib() -> ctypes.CDLL:
         L.thrift_decode_quantize_cache.restype = ctypes.c_int
         L.thrift_decode_step.argtypes = [DSP, P, P, P, DCP, P, P, P, S, P]
         L.thrift_decode_step.restype = ctypes.c_int
+        I64, KSP, KCP = ctypes.c_int64, ctypes.POINTER(Kv8Shape), ctypes.POINTER(Kv8CacheStruct)
+        KMP = ctypes.POINTER(Kv8Mask)
+        L.thrift_kv8_cache_bytes.argtypes = [I32, I32, I32, I32, ctypes.c_int]
+        L.thrift_kv8_cache_bytes.restype = S
+        L.thrift_kv8_append.argtypes = [KSP, KCP, P, I64, P, I64, P, P, P, P]
+        L.thrift_kv8_append.restype = ctypes.c_int
+        L.thrift_kv8_attn_workspace_bytes.argtypes = [KSP, KMP, ctypes.c_int]
+        L.thrift_kv8_attn_workspace_bytes.restype = S
+        L.thrift_kv8_attn.argtypes = [KSP, KMP, KCP, P, I64, P, P, P, P, P, P, I64, P, S, P]
+        L.thrift_kv8_attn.restype = ctypes.c_int
+        L.thrift_kv8_evict.argtypes = [KSP, KCP, P, P, P, I64, I32, I32, I32, KCP, P, I32, P, P, I64, P, P]
+        L.thrift_kv8_evict.restype = ctypes.c_int
         L.thrift_probe_mma.argtypes = [I32, I32, I32, I32, ctypes.POINTER(ctypes.c_float), P, P]
         L.thrift_probe_mma.restype = ctypes.c_int
         L.thrift_launch_count.argtypes = []
@@ -394,6 +420,201 @@ def decode_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cache: dict, 
     _check(lib().thrift_decode_step(ctypes.byref(shape), _ptr(q), _ptr(k), _ptr(v), ctypes.byref(st), _ptr(o),
                                     _ptr(lse), _ptr(ws), ws.numel(), _stream()), "thrift_decode_step")
     return o, lse
+
+
+# ---------------------------------------------------------------------------
+# The paged 8-bit cache.  These calls run once per layer and token, so their checks
+# touch each tensor once; they follow the tensors' device, not the current one.
+# ---------------------------------------------------------------------------
+_KV8_DTYPES = {torch.bfloat16: 0, torch.float16: 1}
+
+
+class Kv8Cache:
+    """A pool of 8-bit pages: k, v uint8 [num_pages, Hkv, page, d] (e4m3 codes), ks, vs uint8
+    [num_pages, Hkv] (the exponent of a page and kv head, plus 127)."""
+
+    __slots__ = ("k", "v", "ks", "vs", "num_pages", "Hkv", "page", "d", "device", "_struct")
+
+    def __init__(self, k: torch.Tensor, v: torch.Tensor, ks: torch.Tensor, vs: torch.Tensor):
+        if not isinstance(k, torch.Tensor) or k.dim() != 4:
+            raise ValueError("k: expected a [num_pages, Hkv, page, d] tensor")
+        _want(k, "k", torch.uint8)
+        _want(v, "v", torch.uint8, tuple(k.shape), k.device)
+        _want(ks, "ks", torch.uint8, tuple(k.shape[:2]), k.device)
+        _want(vs, "vs", torch.uint8, tuple(k.shape[:2]), k.device)
+        self.k, self.v, self.ks, self.vs = k, v, ks, vs
+        self.num_pages, self.Hkv, self.page, self.d = (int(x) for x in k.shape)
+        if int(lib().thrift_kv8_cache_bytes(self.num_pages, self.Hkv, self.page, self.d, 0)) == 0:
+            raise ThriftError(THRIFT_ERR_UNSUPPORTED, "thrift_kv8_cache_bytes")
+        self.device = k.device
+        self._struct = Kv8CacheStruct(k.data_ptr(), v.data_ptr(), ks.data_ptr(), vs.data_ptr(), self.num_pages)
+
+
+def kv8_alloc(num_pages: int, Hkv: int, page: int, d: int, device) -> Kv8Cache:
+    """An empty pool of pages."""
+    k = torch.empty((num_pages, Hkv, page, d), dtype=torch.uint8, device=device)
+    ks = torch.empty((num_pages, Hkv), dtype=torch.uint8, device=device)
+    return Kv8Cache(k, torch.empty_like(k), ks, torch.empty_like(ks))
+
+
+def _kv8_tokens(x: torch.Tensor, name: str, heads: int, d: int, device) -> int:
+    """Checks packed rows [n, heads, d] whose tokens may be strided; returns the token stride."""
+    if not isinstance(x, torch.Tensor) or x.dim() != 3:
+        raise ValueError(f"{name}: expected a [n, heads, d] tensor")
+    if x.dtype not in _KV8_DTYPES:
+        raise ValueError(f"{name}: dtype {x.dtype}, expected torch.bfloat16 or torch.float16")
+    n, h, w = x.shape
+    if w != d or (heads and h != heads):
+        raise ValueError(f"{name}: shape {tuple(x.shape)}, expected (n, {heads or 'Hq'}, {d})")
+    st, sh, sd = x.stride()
+    if n > 0 and (sd != 1 or (sh != d and h != 1) or (st % 8 and n != 1)):
+        raise ValueError(f"{name}: heads and channels must be contiguous and the token stride a multiple of 8")
+    _on_device(x, name, device)
+    return h * d if n <= 1 else st
+
+
+def _kv8_ints(t: torch.Tensor, name: str, shape, device) -> int:
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch.Tensor")
+    if t.dtype is not torch.int32 or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous torch.int32 tensor of shape {tuple(shape)}, "
+                         f"got {t.dtype} {tuple(t.shape)}")
+    _on_device(t, name, device)
+    return t.data_ptr()
+
+
+def _kv8_shape(cache: Kv8Cache, table, lens, cu, n, Hq, max_q, max_len, dtype):
+    """The shape struct and the pointers of table, lens and cu."""
+    if not isinstance(cache, Kv8Cache):
+        raise TypeError("cache: expected a Kv8Cache")
+    if not isinstance(table, torch.Tensor) or table.dim() != 2:
+        raise ValueError("table: expected a [B, pages] tensor")
+    B, cols = table.shape
+    dev = cache.device
+    tp = _kv8_ints(table, "table", (B, cols), dev)
+    lp = _kv8_ints(lens, "lens", (B,), dev)
+    cp = None if cu is None else _kv8_ints(cu, "cu", (B + 1,), dev)
+    if cu is None and n != B:
+        raise ValueError(f"{n} rows for {B} sequences: without cu each sequence has one new token")
+    max_q = (1 if cu is None else n) if max_q is None else int(max_q)
+    max_len = cols * cache.page if max_len is None else int(max_len)
+    return Kv8Shape(B, Hq, cache.Hkv, cache.d, cache.page, cols, n, max_q, max_len, dtype), tp, lp, cp
+
+
+def _kv8_call(fn, what: str, device, *args) -> None:
+    """The call on the device's current stream, with the device current while it launches."""
+    if device.type == "cuda" and device.index != torch.cuda.current_device():
+        with torch.cuda.device(device):
+            status = fn(*args, torch.cuda.current_stream(device).cuda_stream)
+    else:
+        status = fn(*args, _stream())
+    if status != THRIFT_OK:
+        raise ThriftError(status, what)
+
+
+def kv8_append(cache: Kv8Cache, k: torch.Tensor, v: torch.Tensor, table: torch.Tensor, lens: torch.Tensor,
+               cu: Optional[torch.Tensor] = None, max_q: Optional[int] = None) -> None:
+    """thrift_kv8_append: quantise the new tokens k, v [n, Hkv, d] (bf16 or fp16, tokens may be strided) into
+    the pages of their sequences.  table int32 [B, pages]; lens int32 [B], the new tokens included; cu int32
+    [B + 1], sequence b's rows being cu[b] .. cu[b + 1] (None: one token each); max_q bounds a sequence's new
+    tokens (default n, or 1 without cu)."""
+    ks = _kv8_tokens(k, "k", cache.Hkv, cache.d, cache.device)
+    vs = _kv8_tokens(v, "v", cache.Hkv, cache.d, cache.device)
+    if v.dtype is not k.dtype or v.shape != k.shape:
+        raise ValueError("v: expected the dtype and shape of k")
+    shape, tp, lp, cp = _kv8_shape(cache, table, lens, cu, k.shape[0], cache.Hkv, max_q, None, _KV8_DTYPES[k.dtype])
+    _kv8_call(lib().thrift_kv8_append, "thrift_kv8_append", cache.device, ctypes.byref(shape),
+              ctypes.byref(cache._struct), k.data_ptr(), ks, v.data_ptr(), vs, tp, lp, cp)
+
+
+def _kv8_weights(w: torch.Tensor, name: str, B: int, Hkv: int, device) -> int:
+    if not isinstance(w, torch.Tensor) or w.dim() != 3 or w.shape[0] != B or w.shape[1] != Hkv:
+        raise ValueError(f"{name}: expected a [B, Hkv, columns] tensor for B = {B}, Hkv = {Hkv}")
+    if w.dtype is not torch.float32 or not w.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous torch.float32 tensor")
+    _on_device(w, name, device)
+    return w.shape[2]
+
+
+def kv8_attention(q: torch.Tensor, cache: Kv8Cache, table: torch.Tensor, lens: torch.Tensor,
+                  cu: Optional[torch.Tensor] = None, max_q: Optional[int] = None, max_len: Optional[int] = None,
+                  window: int = 0, sinks: int = 0, softmax_scale: float = 0.0,
+                  weights: Optional[torch.Tensor] = None, o: Optional[torch.Tensor] = None,
+                  lse: Optional[torch.Tensor] = None, want_lse: bool = False, ws: Optional[torch.Tensor] = None):
+    """thrift_kv8_attn: attention of the new tokens' queries q [n, Hq, d] (bf16 or fp16, tokens may be strided)
+    over the cache that already holds those tokens -> (o [n, Hq, d], lse fp32 [n, Hq] or None).  Causal; with
+    window > 0 a query at position p sees t > p - window and the first `sinks` tokens.  table, lens, cu, max_q as
+    for kv8_append; max_len bounds lens (default: what the table holds).  weights: fp32 [B, Hkv, >= max_len], to
+    which each token's attention weights are added."""
+    qs = _kv8_tokens(q, "q", 0, cache.d, cache.device)
+    n, Hq, d = q.shape
+    shape, tp, lp, cp = _kv8_shape(cache, table, lens, cu, n, Hq, max_q, max_len, _KV8_DTYPES[q.dtype])
+    dev = cache.device
+    mask = Kv8Mask(window, sinks, softmax_scale)
+    w_cols = 0
+    if weights is not None:
+        w_cols = _kv8_weights(weights, "weights", shape.B, cache.Hkv, dev)
+    if o is None:
+        o = torch.empty((n, Hq, d), dtype=q.dtype, device=dev)
+    else:
+        _want(o, "o", q.dtype, (n, Hq, d), dev)
+    if lse is not None:
+        _want(lse, "lse", torch.float32, (n, Hq), dev)
+    elif want_lse:
+        lse = torch.empty((n, Hq), dtype=torch.float32, device=dev)
+    need = int(lib().thrift_kv8_attn_workspace_bytes(ctypes.byref(shape), ctypes.byref(mask), weights is not None))
+    if ws is not None:
+        _want(ws, "ws", torch.uint8, device=dev)
+        if ws.numel() < need:
+            raise ValueError(f"ws: {ws.numel()} bytes, the call needs {need}")
+    elif need:
+        ws = torch.empty(need, dtype=torch.uint8, device=dev)
+    _kv8_call(lib().thrift_kv8_attn, "thrift_kv8_attn", dev, ctypes.byref(shape), ctypes.byref(mask),
+              ctypes.byref(cache._struct), q.data_ptr(), qs, tp, lp, cp, o.data_ptr(), _ptr(lse), _ptr(weights),
+              w_cols, _ptr(ws), 0 if ws is None else ws.numel())
+    return o, lse
+
+
+def kv8_attention_workspace(q: torch.Tensor, cache: Kv8Cache, table: torch.Tensor, lens: torch.Tensor,
+                            cu: Optional[torch.Tensor] = None, max_q: Optional[int] = None,
+                            max_len: Optional[int] = None, window: int = 0, sinks: int = 0,
+                            weights: Optional[torch.Tensor] = None) -> int:
+    """thrift_kv8_attn_workspace_bytes of a kv8_attention call with these arguments."""
+    _kv8_tokens(q, "q", 0, cache.d, cache.device)
+    shape = _kv8_shape(cache, table, lens, cu, q.shape[0], q.shape[1], max_q, max_len, _KV8_DTYPES[q.dtype])[0]
+    mask = Kv8Mask(window, sinks, 0.0)
+    return int(lib().thrift_kv8_attn_workspace_bytes(ctypes.byref(shape), ctypes.byref(mask), weights is not None))
+
+
+def kv8_evict(cache: Kv8Cache, table: torch.Tensor, lens: torch.Tensor, weights: torch.Tensor, dst: Kv8Cache,
+              dst_table: torch.Tensor, dst_weights: torch.Tensor, keep: int, sinks: int = 0, recent: int = 0,
+              max_len: Optional[int] = None, dst_lens: Optional[torch.Tensor] = None,
+              kept: Optional[torch.Tensor] = None):
+    """thrift_kv8_evict: copy every sequence's and kv head's `keep` tokens with the largest weights (the first
+    `sinks` and the last `recent` always among them) to the pages dst_table of dst -> (dst_lens int32 [B], kept
+    int32 [B, Hkv, keep], the old positions, -1 past the last).  dst may be `cache` if its pages dst_table are
+    none that the call reads; dst_weights must not overlap weights."""
+    shape, tp, lp, _ = _kv8_shape(cache, table, lens, None, table.shape[0], cache.Hkv, 1, max_len, 0)
+    dev, B, Hkv = cache.device, shape.B, cache.Hkv
+    if not isinstance(dst, Kv8Cache) or (dst.Hkv, dst.page, dst.d, dst.device) != (Hkv, cache.page, cache.d, dev):
+        raise ValueError("dst: expected a Kv8Cache with the heads, page, d and device of cache")
+    if not isinstance(dst_table, torch.Tensor) or dst_table.dim() != 2:
+        raise ValueError("dst_table: expected a [B, pages] tensor")
+    dtp = _kv8_ints(dst_table, "dst_table", (B, dst_table.shape[1]), dev)
+    w_cols = _kv8_weights(weights, "weights", B, Hkv, dev)
+    dw_cols = _kv8_weights(dst_weights, "dst_weights", B, Hkv, dev)
+    a, b = weights.data_ptr(), dst_weights.data_ptr()
+    if a < b + 4 * dst_weights.numel() and b < a + 4 * weights.numel():
+        raise ValueError("dst_weights: must not overlap weights")
+    keep = int(keep)
+    if dst_lens is None:
+        dst_lens = torch.empty((B,), dtype=torch.int32, device=dev)
+    if kept is None:
+        kept = torch.empty((B, Hkv, max(keep, 0)), dtype=torch.int32, device=dev)
+    _kv8_call(lib().thrift_kv8_evict, "thrift_kv8_evict", dev, ctypes.byref(shape), ctypes.byref(cache._struct), tp,
+              lp, a, w_cols, keep, int(sinks), int(recent), ctypes.byref(dst._struct), dtp, dst_table.shape[1],
+              _kv8_ints(dst_lens, "dst_lens", (B,), dev), b, dw_cols, _kv8_ints(kept, "kept", (B, Hkv, keep), dev))
+    return dst_lens, kept
 
 
 def device_status() -> tuple:

@@ -288,13 +288,147 @@ thrift_status thrift_decode_step(const thrift_decode_shape* shape, const void* q
   return launch_decode_step(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? THRIFT_OK : THRIFT_ERR_CUDA;
 }
 
+// ---- the paged 8-bit cache
+static int check_pool(int32_t Hkv, int32_t page, int32_t d) {
+  if (Hkv < 1) return THRIFT_ERR_INVALID;
+  if (page != 16 && page != 32 && page != 64 && page != 128) return THRIFT_ERR_UNSUPPORTED;
+  if (d != 64 && d != 128) return THRIFT_ERR_UNSUPPORTED;
+  return 0;
+}
+
+size_t thrift_kv8_cache_bytes(int32_t num_pages, int32_t Hkv, int32_t page, int32_t d, int field) {
+  if (num_pages < 1 || num_pages > (1 << 30) || check_pool(Hkv, page, d) != 0) return 0;
+  const size_t heads = (size_t)num_pages * Hkv;
+  switch (field) {
+    case 0: case 1: return heads * page * d;
+    case 2: case 3: return heads;
+    default: return 0;
+  }
+}
+
+static int check_kv8_shape(const thrift_kv8_shape* s, bool with_q) {
+  if (s == nullptr) return THRIFT_ERR_INVALID;
+  if (s->B < 1 || s->table_cols < 1 || s->n < 0 || s->max_q < 0 || s->max_len < 1) return THRIFT_ERR_INVALID;
+  if (const int e = check_pool(s->Hkv, s->page, s->d)) return e;
+  if (s->dtype != THRIFT_BF16 && s->dtype != THRIFT_FP16) return THRIFT_ERR_INVALID;
+  if (with_q && (s->Hq < 1 || s->Hq % s->Hkv != 0)) return THRIFT_ERR_INVALID;
+  const long long cap = (long long)s->table_cols * s->page;
+  if (s->max_len > cap || s->max_q > s->n) return THRIFT_ERR_INVALID;
+  if (cap > (1 << 24) || (long long)s->B * s->Hkv > 65535) return THRIFT_ERR_UNSUPPORTED;
+  if (with_q && (long long)s->n * s->Hq > 0x7FFFFFFFLL) return THRIFT_ERR_UNSUPPORTED;
+  // the kernels' grids: rows of a sequence (new tokens times query heads of a group), kv heads twice
+  if (with_q && (long long)s->max_q * (s->Hq / s->Hkv) > (1 << 24)) return THRIFT_ERR_UNSUPPORTED;
+  if (2LL * s->Hkv > 65535) return THRIFT_ERR_UNSUPPORTED;
+  return 0;
+}
+
+static bool aligned4(const void* p) { return p != nullptr && (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+static bool null_or_aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+static bool kv8_cache_ok(const thrift_kv8_cache* c) {
+  return c != nullptr && aligned16(c->k) && aligned16(c->v) && c->ks != nullptr && c->vs != nullptr && c->num_pages >= 1 &&
+         c->num_pages <= (1 << 30);
+}
+
+static Kv8Args kv8_args(const thrift_kv8_shape* s, const thrift_kv8_cache* c, const int32_t* table, const int32_t* lens,
+                        const int32_t* cu) {
+  Kv8Args a;
+  a.s = *s;
+  a.cache = *c;
+  a.table = table;
+  a.lens = lens;
+  a.cu = cu;
+  return a;
+}
+
+// cu NULL stands for one new token per sequence.
+static bool kv8_rows_ok(const thrift_kv8_shape* s, const int32_t* cu) {
+  return cu != nullptr ? null_or_aligned4(cu) : (s->n == s->B && s->max_q >= 1);
+}
+
+thrift_status thrift_kv8_append(const thrift_kv8_shape* shape, const thrift_kv8_cache* cache, const void* k,
+                                int64_t k_stride, const void* v, int64_t v_stride, const int32_t* table,
+                                const int32_t* lens, const int32_t* cu, void* stream) {
+  int e = check_kv8_shape(shape, false);
+  if (e) return (thrift_status)e;
+  if (!kv8_cache_ok(cache) || !aligned4(table) || !aligned4(lens) || !kv8_rows_ok(shape, cu)) return THRIFT_ERR_INVALID;
+  if (shape->n == 0 || shape->max_q == 0) return THRIFT_OK;
+  const int64_t row = (int64_t)shape->Hkv * shape->d;
+  if (!aligned16(k) || !aligned16(v) || k_stride < row || v_stride < row || k_stride % 8 != 0 || v_stride % 8 != 0)
+    return THRIFT_ERR_INVALID;
+  const Kv8Args a = kv8_args(shape, cache, table, lens, cu);
+  return launch_kv8_append(a, k, k_stride, v, v_stride, static_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? THRIFT_OK : THRIFT_ERR_CUDA;
+}
+
+static int check_kv8_mask(const thrift_kv8_mask* m) {
+  if (m == nullptr || m->window < 0 || m->sinks < 0) return THRIFT_ERR_INVALID;
+  if (!(m->softmax_scale >= 0.0f) || std::isinf(m->softmax_scale)) return THRIFT_ERR_INVALID;
+  return 0;
+}
+
+size_t thrift_kv8_attn_workspace_bytes(const thrift_kv8_shape* shape, const thrift_kv8_mask* mask, int with_w) {
+  if (check_kv8_shape(shape, true) != 0 || check_kv8_mask(mask) != 0 || shape->n == 0 || shape->max_q == 0) return 0;
+  return kv8_attn_workspace(*shape, *mask, with_w != 0);
+}
+
+thrift_status thrift_kv8_attn(const thrift_kv8_shape* shape, const thrift_kv8_mask* mask, const thrift_kv8_cache* cache,
+                              const void* q, int64_t q_stride, const int32_t* table, const int32_t* lens,
+                              const int32_t* cu, void* o, float* lse, float* w, int64_t w_cols, void* ws,
+                              size_t ws_bytes, void* stream) {
+  int e = check_kv8_shape(shape, true);
+  if (e) return (thrift_status)e;
+  if ((e = check_kv8_mask(mask))) return (thrift_status)e;
+  if (!kv8_cache_ok(cache) || !aligned4(table) || !aligned4(lens) || !kv8_rows_ok(shape, cu) || !null_or_aligned4(lse))
+    return THRIFT_ERR_INVALID;
+  if (w != nullptr && (!aligned16(w) || w_cols < shape->max_len)) return THRIFT_ERR_INVALID;
+  if (shape->n == 0 || shape->max_q == 0) return THRIFT_OK;
+  if (!aligned16(q) || !aligned16(o) || q_stride < (int64_t)shape->Hq * shape->d || q_stride % 8 != 0)
+    return THRIFT_ERR_INVALID;
+  const size_t need = kv8_attn_workspace(*shape, *mask, w != nullptr);
+  if (need > 0 && (!aligned16(ws) || ws_bytes < need)) return THRIFT_ERR_INVALID;
+  Kv8Attn t;
+  t.mask = *mask;
+  t.q = q; t.q_stride = q_stride;
+  t.o = o; t.lse = lse; t.w = w; t.w_cols = w_cols; t.ws = ws;
+  const Kv8Args a = kv8_args(shape, cache, table, lens, cu);
+  return launch_kv8_attn(a, t, static_cast<cudaStream_t>(stream)) == cudaSuccess ? THRIFT_OK : THRIFT_ERR_CUDA;
+}
+
+thrift_status thrift_kv8_evict(const thrift_kv8_shape* shape, const thrift_kv8_cache* cache, const int32_t* table,
+                               const int32_t* lens, const float* w, int64_t w_cols, int32_t keep, int32_t sinks,
+                               int32_t recent, const thrift_kv8_cache* dst, const int32_t* dst_table, int32_t dst_cols,
+                               int32_t* dst_lens, float* dst_w, int64_t dst_w_cols, int32_t* kept, void* stream) {
+  int e = check_kv8_shape(shape, false);
+  if (e) return (thrift_status)e;
+  if (!kv8_cache_ok(cache) || !kv8_cache_ok(dst) || !aligned4(table) || !aligned4(lens) || !aligned4(dst_table) ||
+      !aligned4(dst_lens) || !aligned4(kept) || !aligned16(w) || !aligned16(dst_w))
+    return THRIFT_ERR_INVALID;
+  if (keep < 1 || sinks < 0 || recent < 0 || (int64_t)sinks + recent > keep) return THRIFT_ERR_INVALID;
+  const int64_t most = keep < shape->max_len ? keep : shape->max_len;
+  if (w_cols < shape->max_len || dst_w_cols < most || dst_cols < 1 || (int64_t)dst_cols * shape->page < most)
+    return THRIFT_ERR_INVALID;
+  Kv8Evict v;
+  v.w = w; v.w_cols = w_cols; v.dst_w_cols = dst_w_cols;
+  v.keep = keep; v.sinks = sinks; v.recent = recent; v.dst_cols = dst_cols;
+  v.dst = *dst;
+  v.dst_table = dst_table; v.dst_lens = dst_lens; v.kept = kept; v.dst_w = dst_w;
+  const Kv8Args a = kv8_args(shape, cache, table, lens, nullptr);
+  return launch_kv8_evict(a, v, static_cast<cudaStream_t>(stream)) == cudaSuccess ? THRIFT_OK : THRIFT_ERR_CUDA;
+}
+
 thrift_status thrift_device_status(void* stream, uint32_t* detail) {
   uint32_t w = 0, wd = 0;
   if (read_and_clear_device_error(static_cast<cudaStream_t>(stream), &w) != cudaSuccess) return THRIFT_ERR_CUDA;
   if (read_and_clear_decode_error(&wd) != cudaSuccess) return THRIFT_ERR_CUDA;
   w |= wd << 8;
+  uint32_t wk = 0, wa = 0;
+  if (read_and_clear_kv8_error(&wk) != cudaSuccess) return THRIFT_ERR_CUDA;
+  if (read_and_clear_kv8_attn_error(&wa) != cudaSuccess) return THRIFT_ERR_CUDA;
+  w |= (wk | wa) << 16;
   if (detail != nullptr) *detail = w;
-  return w != 0 ? THRIFT_ERR_TIMEOUT : THRIFT_OK;
+  if ((w & ~0x10000u) != 0) return THRIFT_ERR_TIMEOUT;
+  return w != 0 ? THRIFT_ERR_INVALID : THRIFT_OK;
 }
 
 thrift_status thrift_debug_withhold_v_load(int32_t tile) {

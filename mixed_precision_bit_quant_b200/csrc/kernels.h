@@ -66,6 +66,39 @@ cudaError_t read_and_clear_decode_error(uint32_t* word);
 
 cudaError_t read_and_clear_device_error(cudaStream_t s, uint32_t* word);
 
+// The paged 8-bit cache.  Arguments are checked by the C ABI layer.
+struct Kv8Args {
+  thrift_kv8_shape s;
+  thrift_kv8_cache cache;
+  const int32_t *table, *lens, *cu;
+};
+struct Kv8Attn {
+  thrift_kv8_mask mask;
+  const void* q;
+  int64_t q_stride;
+  void* o;
+  float *lse, *w;
+  int64_t w_cols;
+  void* ws;
+};
+struct Kv8Evict {
+  const float* w;
+  int64_t w_cols, dst_w_cols;
+  int32_t keep, sinks, recent, dst_cols;
+  thrift_kv8_cache dst;
+  const int32_t* dst_table;
+  int32_t *dst_lens, *kept;
+  float* dst_w;
+};
+cudaError_t launch_kv8_append(const Kv8Args& a, const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                              cudaStream_t s);
+size_t kv8_attn_workspace(const thrift_kv8_shape& s, const thrift_kv8_mask& m, bool with_w);
+cudaError_t launch_kv8_attn(const Kv8Args& a, const Kv8Attn& t, cudaStream_t s);
+cudaError_t launch_kv8_evict(const Kv8Args& a, const Kv8Evict& e, cudaStream_t s);
+// bit 0: a bad length, range or page number; bit 1: a wait that ran out
+cudaError_t read_and_clear_kv8_error(uint32_t* word);
+cudaError_t read_and_clear_kv8_attn_error(uint32_t* word);
+
 // Tensor-core rate probe (returns a thrift_status); cycles_dev: [ctas] per-CTA clock counts.
 int launch_mma_probe(int kind, int n, int iters, int ctas, float* ms, unsigned long long* cycles_dev,
                      cudaStream_t st);

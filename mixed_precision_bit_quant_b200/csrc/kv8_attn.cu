@@ -1,0 +1,620 @@
+// Attention over the paged 8-bit cache: causal, with an optional sliding window and
+// first tokens that stay visible, for any number of new tokens per sequence.
+// HyQuant: Hybrid-Precision Quantization for LLM Attention (abstract, decode
+// stage): the dequantisation is fused into the attention over the compressed
+// cache; sink tokens and the local window are what a windowed call keeps.
+//
+// The query rows of one kv head's group are taken together: row r = i * G + g is
+// query head hk * G + g of new token i.  Kernels:
+//   split_kernel   one CTA per (tile of 8 or 16 rows, run of visible tokens, sequence and kv
+//                  head): online softmax over the run; writes the output, or the run's
+//                  state (maximum, sum, unnormalised output) when there are several runs
+//   merge_kernel   joins the runs' states of a row
+//   weights_kernel adds the rows' final weights to the running sums of the tokens
+#include "kv8.cuh"
+
+namespace thrift {
+namespace kv8 {
+
+constexpr int kTile = 16;         // tokens of a warp's step (the m16 of its products)
+constexpr int kSplitThreads = 128;
+constexpr int kSplitWarps = kSplitThreads / 32;
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.69314718055994531f;
+
+struct AttnParams {
+  const uint8_t *k, *v, *ks, *vs;
+  const void* q;
+  long long q_stride;  // elements
+  const int32_t *table, *lens, *cu;
+  void* o;
+  float* lse;
+  float2* part_ml;  // [row][nsplit] maximum (log2 domain) and sum
+  float* part_o;    // [row][nsplit][D]
+  float* lse2;      // [row] log2-domain log-sum-exp for the weights (or null)
+  float* w;
+  long long w_cols;
+  int Hq, Hkv, G, page_log2, table_cols, n, max_q, max_len, num_pages, window, sinks, fp16;
+  int nsplit, chunk, row_tiles;  // chunk: 16-token tiles of a run
+  float scale_log2;
+};
+
+// D[16x8] += A[16x16] B[16x8], FP16 operands, FP32 accumulation.  Fragments (two FP16 per
+// register, the lower k in the low half; g = lane / 4, t = lane % 4): a0 (row g, k 2t, 2t+1),
+// a1 (row g+8, same k), a2 (row g, k 2t+8, +9), a3 (row g+8, same); b0 (k 2t, 2t+1, col g),
+// b1 (k 2t+8, +9, col g); d0, d1 (row g, cols 2t, 2t+1), d2, d3 (row g+8).
+__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// Transpose of an 8x8 matrix of 16-bit values held as fragments (row g, cols 2t, 2t+1).
+__device__ __forceinline__ uint32_t movmatrix(uint32_t x) {
+  uint32_t r;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
+}
+
+// The tokens that a tile of query rows can see, as an index space of 16-token tiles:
+// [0, s_tiles) are the sinks' tiles, the rest start at tile a_tile.
+struct Span {
+  int s_tiles, a_tile, count;
+  __device__ __forceinline__ int token(int v) const { return (v < s_tiles ? v : a_tile + (v - s_tiles)) * kTile; }
+};
+__device__ __forceinline__ Span visible_span(int p_lo, int p_hi, int window, int sinks) {
+  Span s{0, 0, 0};
+  if (p_hi < 0) return s;
+  if (window > 0) {
+    const int a = max(0, p_lo - window + 1) / kTile;
+    const int z = (min(sinks, p_hi + 1) + kTile - 1) / kTile;
+    if (a > z) {
+      s.s_tiles = z;
+      s.a_tile = a;
+    }
+  }
+  s.count = s.s_tiles + (p_hi + kTile) / kTile - s.a_tile;
+  return s;
+}
+
+// A row's log-sum-exp from its maximum (log2 domain) and sum.
+__device__ __forceinline__ void write_lse(const AttnParams& p, long long row, float m, float l) {
+  const float x = l > 0.0f ? m + log2f(l) : -INFINITY;
+  if (p.lse != nullptr) p.lse[row] = x * kLn2;
+  if (p.lse2 != nullptr) p.lse2[row] = x;
+}
+
+// Row r's packed index (token * Hq + head).
+__device__ __forceinline__ long long packed_row(const AttnParams& p, const Seq& s, int hk, int r) {
+  return (long long)(s.q0 + r / p.G) * p.Hq + hk * p.G + r % p.G;
+}
+__device__ __forceinline__ const uint32_t* query_row(const AttnParams& p, const Seq& s, int hk, int r, int d) {
+  const uint16_t* q = static_cast<const uint16_t*>(p.q) + (long long)(s.q0 + r / p.G) * p.q_stride + (hk * p.G + r % p.G) * d;
+  return reinterpret_cast<const uint32_t*>(q);
+}
+
+// Query row `r` as the FP16 B fragments of the logits' products, times 2^-e with
+// e = floor(log2 amax) - 14: its largest component lands in [2^14, 2^15), so a component
+// is exact unless it is 2^31 (BF16) or 2^28 (FP16) times smaller, and then at most 2^-39 of
+// the largest is lost.  Step s pairs k = 2t, 2t+1 and 2t+8, 2t+9 with four
+// consecutive channels, 64 (s / 4) + 16 t + 4 (s % 4) and up, so that a lane's codes of a token
+// are whole 16-byte vectors.  The row's four lanes (t = 0..3) share e; returns it.
+template <int D>
+__device__ __forceinline__ int load_query(const uint32_t* q, int t, bool fp16, uint32_t (&f)[D / 16][2]) {
+  uint32_t am = 0;
+#pragma unroll
+  for (int v = 0; v < D / 64; ++v)
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      uint4 u = make_uint4(0, 0, 0, 0);
+      if (q != nullptr) u = __ldg(reinterpret_cast<const uint4*>(q + 32 * v + 8 * t + 4 * x));
+      f[4 * v + 2 * x][0] = u.x;
+      f[4 * v + 2 * x][1] = u.y;
+      f[4 * v + 2 * x + 1][0] = u.z;
+      f[4 * v + 2 * x + 1][1] = u.w;
+    }
+#pragma unroll
+  for (int i = 0; i < D / 16; ++i) am = __vmaxu2(am, __vmaxu2(f[i][0] & 0x7FFF7FFFu, f[i][1] & 0x7FFF7FFFu));
+  am = max(am & 0xFFFFu, am >> 16);
+  am = max(am, __shfl_xor_sync(0xffffffffu, am, 1));
+  am = max(am, __shfl_xor_sync(0xffffffffu, am, 2));
+  const int ex = (int)(__float_as_uint(pair_to_float2(am, fp16).x) >> 23) - 127;
+  const int e = max(-100, ex - 14);
+  const float down = pow2f(-e);
+#pragma unroll
+  for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      const float2 a = pair_to_float2(f[i][x], fp16);
+      const __half2 h = __floats2half2_rn(a.x * down, a.y * down);
+      f[i][x] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+  return e;
+}
+
+// The codes of a tile of 16 tokens as a lane loads them.  K: of tokens g and g+8 the 16
+// channels from 16 t (and from 64 + 16 t); V: of tokens 2t, 2t+1, 2t+8, 2t+9 the D/8 channels from g D/8.
+// A warp's load covers whole 32-byte sectors of a token's row in both.
+template <int D>
+struct Codes {
+  uint4 k[2][D / 64];
+  uint32_t v[4][D / 32];
+};
+
+template <int D>
+__device__ __forceinline__ void load_k(const uint8_t* kp, int g, int t, uint4 (&k)[2][D / 64]) {
+#pragma unroll
+  for (int r = 0; r < 2; ++r)
+#pragma unroll
+    for (int x = 0; x < D / 64; ++x) k[r][x] = __ldg(reinterpret_cast<const uint4*>(kp + (g + 8 * r) * D + 64 * x + 16 * t));
+}
+template <int D>
+__device__ __forceinline__ void load_v(const uint8_t* vp, int g, int t, uint32_t (&v)[4][D / 32]) {
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    const uint8_t* a = vp + (2 * t + (r & 1) + 8 * (r >> 1)) * D + g * (D / 8);
+    if constexpr (D == 128) {
+      const uint4 u = __ldg(reinterpret_cast<const uint4*>(a));
+      v[r][0] = u.x; v[r][1] = u.y; v[r][2] = u.z; v[r][3] = u.w;
+    } else {
+      const uint2 u = __ldg(reinterpret_cast<const uint2*>(a));
+      v[r][0] = u.x; v[r][1] = u.y;
+    }
+  }
+}
+
+__device__ __forceinline__ uint32_t word_of(const uint4& u, int i) { return i == 0 ? u.x : i == 1 ? u.y : i == 2 ? u.z : u.w; }
+
+// Raw logits (code units) of 16 tokens x 8 NT rows.
+template <int D, int NT>
+__device__ __forceinline__ void tile_logits(const uint4 (&k)[2][D / 64], const uint32_t (&qf)[NT][D / 16][2], float (&s)[NT][4]) {
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) s[n][e] = 0.0f;
+#pragma unroll
+  for (int i = 0; i < D / 16; ++i) {
+    const uint32_t lo = word_of(k[0][i / 4], i % 4), hi = word_of(k[1][i / 4], i % 4);
+    const uint32_t a0 = e4m3x2_to_h2(lo & 0xFFFFu), a2 = e4m3x2_to_h2(lo >> 16);
+    const uint32_t a1 = e4m3x2_to_h2(hi & 0xFFFFu), a3 = e4m3x2_to_h2(hi >> 16);
+#pragma unroll
+    for (int n = 0; n < NT; ++n) mma16816(s[n], a0, a1, a2, a3, qf[n][i][0], qf[n][i][1]);
+  }
+}
+
+constexpr float kLazy = 4.0f;  // a row's maximum is raised only when exceeded by 2^4
+constexpr int kPShift = 11;    // P enters FP16 times 2^11: at most 2^(4 + 11) = 2^15
+
+// One CTA per (row tile, run of visible tokens; sequence and kv head).  Each warp walks its
+// own tiles of 16 tokens straight from global memory into matrix fragments -- the codes'
+// layout in a page is the fragments' layout, so nothing is staged -- with the next tile's
+// loads in flight, and keeps its own softmax state; the warps' states are joined at the end.
+//   S^T = K Q^T (m = tokens, n = rows): the e4m3 codes are exact in FP16; the page's scale,
+// the row's and the softmax's multiply the FP32 logits.
+//   O^T += V^T P^T: P goes to FP16 as p 2^(e_v - e_ref + 11), where e_v is the page's V exponent and
+// e_ref the largest seen, so the products see bare codes; S's fragment becomes P's by one
+// 8x8 transpose.  A row's maximum is raised (and O rescaled) only when a logit
+// exceeds it by 4 binades: the common step needs one vote and no cross-lane maximum.
+template <int D, int NT>
+__global__ void __launch_bounds__(kSplitThreads) split_kernel(const AttnParams p) {
+  constexpr int R = 8 * NT;
+  const int bk = blockIdx.y, b = bk / p.Hkv, hk = bk % p.Hkv;
+  const int split = blockIdx.x % p.nsplit, rt = blockIdx.x / p.nsplit;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const Seq s = load_seq(p.lens, p.cu, b, p.n, p.max_q, p.max_len);
+  if (s.bad && threadIdx.x == 0 && blockIdx.x == 0 && hk == 0) raise_bad();
+  const int rows = s.nq * p.G - rt * R;  // rows of this tile (may exceed R)
+  if (rows <= 0) return;
+  const int r_base = rt * R, r_cnt = min(rows, R);
+  const int p_lo = s.pos0 + r_base / p.G, p_hi = s.pos0 + (r_base + r_cnt - 1) / p.G;
+  const Span span = visible_span(p_lo, p_hi, p.window, p.sinks);
+  const int v0 = split * p.chunk, v1 = min(span.count, v0 + p.chunk);
+
+  extern __shared__ __align__(16) float sm[];
+  float* so = sm;                              // [warps][R][D + 4]
+  float* sml = sm + kSplitWarps * R * (D + 4);  // [warps][R][2]
+
+  if (v0 >= v1 && (p.nsplit > 1)) {  // nothing in this run: an empty state
+    for (int r = threadIdx.x; r < r_cnt; r += kSplitThreads)
+      p.part_ml[packed_row(p, s, hk, r_base + r) * p.nsplit + split] = make_float2(-INFINITY, 0.0f);
+    return;
+  }
+
+  uint32_t qf[NT][D / 16][2];
+  float fs[NT][2];   // per column 2t, 2t+1: logits' scale without the page's
+  int pos[NT][2];    // per column: the query's position
+  float m[NT][2], l[NT][2];
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+    const int r = 8 * n + g;
+    const int e = load_query<D>(r < r_cnt ? query_row(p, s, hk, r_base + r, D) : nullptr, t, p.fp16, qf[n]);
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      const int ec = __shfl_sync(0xffffffffu, e, 4 * (2 * t + x));
+      fs[n][x] = pow2f(ec) * p.scale_log2;
+      const int c = 8 * n + 2 * t + x;
+      pos[n][x] = c < r_cnt ? s.pos0 + (r_base + c) / p.G : -1;
+      m[n][x] = -INFINITY;
+      l[n][x] = 0.0f;
+    }
+  }
+  float acc[NT][D / 16][4];
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int j = 0; j < D / 16; ++j)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[n][j][e] = 0.0f;
+  int e_ref = -1000;
+
+  const int32_t* trow = p.table + (long long)b * p.table_cols;
+  const int page_mask = (1 << p.page_log2) - 1;
+  int l_page = -1, l_ks = 0, l_vs = 0;  // lane's tile of the current batch of 32 of this warp's tiles
+  const int count = v1 > v0 + warp ? (v1 - v0 - warp + kSplitWarps - 1) / kSplitWarps : 0;
+
+  auto batch = [&](int it0) {
+    const int v = v0 + warp + (it0 + lane) * kSplitWarps;
+    l_page = -1;
+    if (v < v1) {
+      const int pg = __ldg(trow + (span.token(v) >> p.page_log2));
+      if (pg >= 0 && pg < p.num_pages) {
+        l_page = pg;
+        l_ks = __ldg(p.ks + (long long)pg * p.Hkv + hk);
+        l_vs = __ldg(p.vs + (long long)pg * p.Hkv + hk);
+      } else {
+        raise_bad();
+      }
+    }
+  };
+  auto fetch = [&](int it, Codes<D>& c, int& pg) {
+    pg = __shfl_sync(0xffffffffu, l_page, it & 31);
+    if (pg >= 0) {
+      const int tok = span.token(v0 + warp + it * kSplitWarps);
+      const long long off = (((long long)pg * p.Hkv + hk) << p.page_log2) * D + (tok & page_mask) * D;
+      load_k<D>(p.k + off, g, t, c.k);
+      load_v<D>(p.v + off, g, t, c.v);
+    }
+  };
+  auto step = [&](int it, Codes<D>& c, int pg, int ksc, int vsc) {
+    if (pg < 0) return;
+    const int tok = span.token(v0 + warp + it * kSplitWarps);
+    float x[NT][4];
+    tile_logits<D, NT>(c.k, qf, x);
+    const float kscale = scale_value((uint32_t)ksc);
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x[n][e] *= fs[n][e & 1] * kscale;
+    const bool full = tok + kTile - 1 <= p_lo && (p.window == 0 || tok > p_hi - p.window || tok + kTile <= p.sinks);
+    if (!full) {
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int tt = tok + g + 8 * (e >> 1), pp = pos[n][e & 1];
+          const bool see = tt <= pp && (p.window == 0 || tt > pp - p.window || tt < p.sinks);
+          if (!see) x[n][e] = -INFINITY;
+        }
+      // codes of tokens that no row sees may be NaN: a zero probability does not silence them
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int tt = tok + 2 * t + (r & 1) + 8 * (r >> 1);
+        const bool see = tt <= p_hi && (p.window == 0 || tt > p_lo - p.window || tt < p.sinks);
+        if (!see) {
+#pragma unroll
+          for (int y = 0; y < D / 32; ++y) c.v[r][y] = 0u;
+        }
+      }
+    }
+    bool raise = false;
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int y = 0; y < 2; ++y) raise |= fmaxf(x[n][y], x[n][y + 2]) > m[n][y] + kLazy;
+    const int ev = vsc - 127;
+    if (__any_sync(0xffffffffu, raise) || ev > e_ref) {
+      const int e_new = max(ev, e_ref);
+      const float fe = e_ref > -1000 ? pow2f(max(-126, e_ref - e_new)) : 0.0f;
+      e_ref = e_new;
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+          float mm = fmaxf(x[n][y], x[n][y + 2]);
+          mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, 4));
+          mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, 8));
+          mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, 16));
+          const float mn = fmaxf(m[n][y], mm);
+          const float f = m[n][y] == -INFINITY ? 0.0f : ex2_approx(m[n][y] - mn);
+          m[n][y] = mn;
+          l[n][y] *= f;
+#pragma unroll
+          for (int j = 0; j < D / 16; ++j) {
+            acc[n][j][y] *= f * fe;
+            acc[n][j][y + 2] *= f * fe;
+          }
+        }
+    }
+    const float pv = pow2f(max(-126, ev - e_ref + kPShift));
+    uint32_t pb[NT][2];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float mu = m[n][e & 1];
+        x[n][e] = mu == -INFINITY ? 0.0f : ex2_approx(x[n][e] - mu);
+        l[n][e & 1] += x[n][e];
+      }
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
+        const __half2 h = __floats2half2_rn(x[n][2 * y] * pv, x[n][2 * y + 1] * pv);
+        pb[n][y] = movmatrix(*reinterpret_cast<const uint32_t*>(&h));
+      }
+    }
+#pragma unroll
+    for (int w = 0; w < D / 32; ++w) {
+      // words w of four tokens -> channels 4w .. 4w+3 as pairs of tokens
+      const uint32_t a01 = __byte_perm(c.v[0][w], c.v[1][w], 0x5140), a23 = __byte_perm(c.v[0][w], c.v[1][w], 0x7362);
+      const uint32_t b01 = __byte_perm(c.v[2][w], c.v[3][w], 0x5140), b23 = __byte_perm(c.v[2][w], c.v[3][w], 0x7362);
+      const uint32_t a0 = e4m3x2_to_h2(a01 & 0xFFFFu), a1 = e4m3x2_to_h2(a01 >> 16);
+      const uint32_t a2 = e4m3x2_to_h2(b01 & 0xFFFFu), a3 = e4m3x2_to_h2(b01 >> 16);
+      const uint32_t c0 = e4m3x2_to_h2(a23 & 0xFFFFu), c1 = e4m3x2_to_h2(a23 >> 16);
+      const uint32_t c2 = e4m3x2_to_h2(b23 & 0xFFFFu), c3 = e4m3x2_to_h2(b23 >> 16);
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        mma16816(acc[n][2 * w], a0, a1, a2, a3, pb[n][0], pb[n][1]);
+        mma16816(acc[n][2 * w + 1], c0, c1, c2, c3, pb[n][0], pb[n][1]);
+      }
+    }
+  };
+
+  Codes<D> ca, cb;
+  int pa = -1, pbg = -1;
+  if (count > 0) {
+    batch(0);
+    fetch(0, ca, pa);
+  }
+  for (int it = 0; it < count; it += 2) {
+    // the lane that holds a tile's page also holds its scales; a batch is 32 tiles (even)
+    int ksc = __shfl_sync(0xffffffffu, l_ks, it & 31), vsc = __shfl_sync(0xffffffffu, l_vs, it & 31);
+    const int ksc1 = __shfl_sync(0xffffffffu, l_ks, (it + 1) & 31), vsc1 = __shfl_sync(0xffffffffu, l_vs, (it + 1) & 31);
+    if (it + 1 < count) fetch(it + 1, cb, pbg);
+    step(it, ca, pa, ksc, vsc);
+    if (it + 2 < count) {
+      if (((it + 2) & 31) == 0) batch(it + 2);
+      fetch(it + 2, ca, pa);
+    }
+    if (it + 1 < count) step(it + 1, cb, pbg, ksc1, vsc1);
+  }
+
+  // ---- join the warps' states
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int y = 0; y < 2; ++y) {
+      float ll = l[n][y];
+      ll += __shfl_xor_sync(0xffffffffu, ll, 4);
+      ll += __shfl_xor_sync(0xffffffffu, ll, 8);
+      ll += __shfl_xor_sync(0xffffffffu, ll, 16);
+      const int c = 8 * n + 2 * t + y;
+      if (g == 0) {
+        sml[(warp * R + c) * 2] = m[n][y];
+        sml[(warp * R + c) * 2 + 1] = ll;
+      }
+      // back to values: 2^(e_ref - 11) in two steps (e_ref may be -127)
+      const float f1 = count > 0 && e_ref > -1000 ? scale_value((uint32_t)(e_ref + 127)) : 0.0f;
+      const float f2 = 1.0f / (1 << kPShift);
+#pragma unroll
+      for (int j = 0; j < D / 16; ++j)
+        *reinterpret_cast<float2*>(so + (warp * R + c) * (D + 4) + g * (D / 8) + 2 * j) =
+            make_float2(acc[n][j][y] * f2 * f1, acc[n][j][y + 2] * f2 * f1);
+    }
+  __syncthreads();
+  for (int i = threadIdx.x; i < r_cnt * (D / 4); i += kSplitThreads) {
+    const int r = i / (D / 4), c4 = i % (D / 4);
+    float mm = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < kSplitWarps; ++w) mm = fmaxf(mm, sml[(w * R + r) * 2]);
+    float ll = 0.0f;
+    float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+    for (int w = 0; w < kSplitWarps; ++w) {
+      const float mw = sml[(w * R + r) * 2];
+      const float f = mw == -INFINITY ? 0.0f : ex2_approx(mw - mm);
+      const float4 x = *reinterpret_cast<const float4*>(so + (w * R + r) * (D + 4) + 4 * c4);
+      ll += sml[(w * R + r) * 2 + 1] * f;
+      o.x += x.x * f;
+      o.y += x.y * f;
+      o.z += x.z * f;
+      o.w += x.w * f;
+    }
+    const long long row = packed_row(p, s, hk, r_base + r);
+    if (p.nsplit == 1) {
+      const float inv = ll > 0.0f ? 1.0f / ll : 0.0f;
+      reinterpret_cast<uint2*>(p.o)[row * (D / 4) + c4] =
+          make_uint2(float2_to_pair(o.x * inv, o.y * inv, p.fp16), float2_to_pair(o.z * inv, o.w * inv, p.fp16));
+      if (c4 == 0) write_lse(p, row, mm, ll);
+    } else {
+      *reinterpret_cast<float4*>(p.part_o + (row * p.nsplit + split) * D + 4 * c4) = o;
+      if (c4 == 0) p.part_ml[row * p.nsplit + split] = make_float2(mm, ll);
+    }
+  }
+}
+
+// One CTA per new token of a sequence, a warp per query head: the runs' states joined, a
+// lane's D / 32 channels in registers.
+template <int D>
+__global__ void __launch_bounds__(128) merge_kernel(const AttnParams p) {
+  constexpr int C = D / 32;
+  const int lane = threadIdx.x & 31;
+  const Seq s = load_seq(p.lens, p.cu, blockIdx.y, p.n, p.max_q, p.max_len);
+  if ((int)blockIdx.x >= s.nq) return;
+  for (int h = threadIdx.x >> 5; h < p.Hq; h += 4) {
+    const long long row = (long long)(s.q0 + blockIdx.x) * p.Hq + h;
+    const float2* ml = p.part_ml + row * p.nsplit;
+    float mm = -INFINITY;
+    for (int i = lane; i < p.nsplit; i += 32) mm = fmaxf(mm, ml[i].x);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, o));
+    float ll = 0.0f, acc[C];
+#pragma unroll
+    for (int c = 0; c < C; ++c) acc[c] = 0.0f;
+    for (int i = 0; i < p.nsplit; ++i) {
+      const float2 x = ml[i];
+      if (x.x == -INFINITY) continue;  // an empty run wrote no output
+      const float f = ex2_approx(x.x - mm);
+      ll += x.y * f;
+      const float* y = p.part_o + (row * p.nsplit + i) * D + lane * C;
+#pragma unroll
+      for (int c = 0; c < C; ++c) acc[c] += y[c] * f;
+    }
+    const float inv = ll > 0.0f ? 1.0f / ll : 0.0f;
+    uint32_t* o = static_cast<uint32_t*>(p.o) + row * (D / 2) + lane * (C / 2);
+#pragma unroll
+    for (int c = 0; c < C; c += 2) o[c / 2] = float2_to_pair(acc[c] * inv, acc[c + 1] * inv, p.fp16);
+    if (lane == 0) write_lse(p, row, mm, ll);
+  }
+}
+
+// One warp per 16 tokens, over all rows that see them: the logits again, now with the rows'
+// final log-sum-exp, and their weights summed per token.  A token's sum is made by
+// one warp in a fixed order, so it does not depend on how the work is spread.
+template <int D>
+__global__ void __launch_bounds__(128) weights_kernel(const AttnParams p) {
+  const int bk = blockIdx.y, b = bk / p.Hkv, hk = bk % p.Hkv;
+  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const Seq s = load_seq(p.lens, p.cu, b, p.n, p.max_q, p.max_len);
+  const int tok = (blockIdx.x * 4 + (threadIdx.x >> 5)) * kTile;
+  if (tok >= s.len || s.nq == 0) return;
+  // rows of the tokens: positions from tok on, up to the window's end unless they are sinks
+  const int i0 = max(0, tok - s.pos0);
+  int i1 = s.nq;
+  if (p.window > 0 && tok >= p.sinks) i1 = min(i1, tok + kTile - 1 + p.window - s.pos0);
+  if (i0 >= i1) return;
+  const int pg = __ldg(p.table + (long long)b * p.table_cols + (tok >> p.page_log2));
+  if (pg < 0 || pg >= p.num_pages) return;  // reported by the attention
+  const long long ph = (long long)pg * p.Hkv + hk;
+  uint4 k[2][D / 64];
+  load_k<D>(p.k + (ph << p.page_log2) * D + (tok & ((1 << p.page_log2) - 1)) * D, g, t, k);
+  const float kscale = scale_value(__ldg(p.ks + ph));
+  float sum[2] = {0.0f, 0.0f};
+  for (int r0 = i0 * p.G; r0 < i1 * p.G; r0 += 8) {
+    uint32_t qf[1][D / 16][2];
+    const int r = r0 + g;
+    const int e = load_query<D>(r < s.nq * p.G ? query_row(p, s, hk, r, D) : nullptr, t, p.fp16, qf[0]);
+    float x[1][4];
+    tile_logits<D, 1>(k, qf, x);
+#pragma unroll
+    for (int y = 0; y < 2; ++y) {
+      const float f = pow2f(__shfl_sync(0xffffffffu, e, 4 * (2 * t + y))) * p.scale_log2;
+      const int c = r0 + 2 * t + y;
+      if (c < s.nq * p.G) {
+        const float lse2 = p.lse2[packed_row(p, s, hk, c)];
+        const int pp = s.pos0 + c / p.G;
+#pragma unroll
+        for (int z = 0; z < 2; ++z) {
+          const int tt = tok + g + 8 * z;
+          const bool see = tt <= pp && (p.window == 0 || tt > pp - p.window || tt < p.sinks);
+          if (see) sum[z] += ex2_approx(x[0][y + 2 * z] * (f * kscale) - lse2);
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int z = 0; z < 2; ++z) {
+    sum[z] += __shfl_xor_sync(0xffffffffu, sum[z], 1);
+    sum[z] += __shfl_xor_sync(0xffffffffu, sum[z], 2);
+    const int tt = tok + g + 8 * z;
+    if (t == 0 && tt < s.len) p.w[(long long)bk * p.w_cols + tt] += sum[z];
+  }
+}
+
+// How a call is cut up: rows of a tile, runs per row tile.  The same for the workspace's
+// size and the launch.
+struct Plan {
+  int nt, row_tiles, nsplit, chunk;
+  size_t ml_off, o_off, lse_off, bytes;
+};
+static Plan make_plan(const thrift_kv8_shape& s, const thrift_kv8_mask& m, bool with_w) {
+  Plan p;
+  const long long G = s.Hq / s.Hkv, rows = (long long)s.max_q * G;
+  p.nt = rows <= 8 ? 1 : 2;
+  const int R = 8 * p.nt;
+  p.row_tiles = (int)((rows + R - 1) / R);
+  long long span = s.max_len;
+  if (m.window > 0) {
+    const long long w = (long long)m.window + (R + G - 1) / G + 2 * kTile + m.sinks + kTile;
+    if (w < span) span = w;
+  }
+  const long long tiles = (span + kTile - 1) / kTile + 1;
+  const long long units = (long long)s.B * s.Hkv * p.row_tiles;
+  long long ns = (148 * 4) / units;
+  const long long most = (tiles + kSplitWarps - 1) / kSplitWarps;
+  ns = ns < 1 ? 1 : (ns > most ? most : ns);
+  if (ns > 64) ns = 64;
+  p.chunk = (int)(((tiles + ns - 1) / ns + kSplitWarps - 1) / kSplitWarps * kSplitWarps);
+  p.nsplit = (int)((tiles + p.chunk - 1) / p.chunk);
+  const size_t nrow = (size_t)s.n * s.Hq;
+  p.ml_off = 0;
+  p.o_off = p.nsplit > 1 ? (nrow * p.nsplit * sizeof(float2) + 255) / 256 * 256 : 0;
+  p.lse_off = p.nsplit > 1 ? p.o_off + nrow * p.nsplit * s.d * sizeof(float) : 0;
+  p.bytes = p.lse_off + (with_w ? nrow * sizeof(float) : 0);
+  return p;
+}
+
+template <int D, int NT>
+static void launch_split(const AttnParams& p, dim3 grid, cudaStream_t s) {
+  constexpr int sm = (int)sizeof(float) * kSplitWarps * 8 * NT * (D + 4 + 2);
+  split_kernel<D, NT><<<grid, kSplitThreads, sm, s>>>(p);
+}
+
+template <int D>
+static void launch_attn_d(const AttnParams& p, const Plan& plan, const thrift_kv8_shape& s, cudaStream_t st) {
+  const dim3 grid(plan.nsplit * plan.row_tiles, s.B * s.Hkv);
+  int launches = 1;
+  if (plan.nt == 1) launch_split<D, 1>(p, grid, st);
+  else launch_split<D, 2>(p, grid, st);
+  if (plan.nsplit > 1) {
+    merge_kernel<D><<<dim3(s.max_q, s.B), 128, 0, st>>>(p);
+    ++launches;
+  }
+  if (p.w != nullptr) {
+    weights_kernel<D><<<dim3((s.max_len + 4 * kTile - 1) / (4 * kTile), s.B * s.Hkv), 128, 0, st>>>(p);
+    ++launches;
+  }
+  count_launches(launches);
+}
+
+}  // namespace kv8
+
+cudaError_t read_and_clear_kv8_attn_error(uint32_t* word) { return kv8::read_and_clear_word(word); }
+
+size_t kv8_attn_workspace(const thrift_kv8_shape& s, const thrift_kv8_mask& m, bool with_w) {
+  return kv8::make_plan(s, m, with_w).bytes;
+}
+
+cudaError_t launch_kv8_attn(const Kv8Args& a, const Kv8Attn& t, cudaStream_t st) {
+  const kv8::Plan plan = kv8::make_plan(a.s, t.mask, t.w != nullptr);
+  kv8::AttnParams p;
+  p.k = a.cache.k; p.v = a.cache.v; p.ks = a.cache.ks; p.vs = a.cache.vs;
+  p.q = t.q; p.q_stride = t.q_stride;
+  p.table = a.table; p.lens = a.lens; p.cu = a.cu;
+  p.o = t.o; p.lse = t.lse;
+  uint8_t* ws = static_cast<uint8_t*>(t.ws);
+  p.part_ml = reinterpret_cast<float2*>(ws + plan.ml_off);
+  p.part_o = reinterpret_cast<float*>(ws + plan.o_off);
+  p.w = t.w; p.w_cols = t.w_cols;
+  p.lse2 = t.w != nullptr ? reinterpret_cast<float*>(ws + plan.lse_off) : nullptr;
+  p.Hq = a.s.Hq; p.Hkv = a.s.Hkv; p.G = a.s.Hq / a.s.Hkv;
+  p.page_log2 = 31 - __builtin_clz((unsigned)a.s.page);
+  p.table_cols = a.s.table_cols; p.n = a.s.n; p.max_q = a.s.max_q; p.max_len = a.s.max_len;
+  p.num_pages = a.cache.num_pages;
+  p.window = t.mask.window; p.sinks = t.mask.sinks; p.fp16 = a.s.dtype == THRIFT_FP16;
+  p.nsplit = plan.nsplit; p.chunk = plan.chunk; p.row_tiles = plan.row_tiles;
+  const float scale = t.mask.softmax_scale > 0.0f ? t.mask.softmax_scale : 1.0f / sqrtf((float)a.s.d);
+  p.scale_log2 = scale * kv8::kLog2e;
+  if (a.s.d == 128) kv8::launch_attn_d<128>(p, plan, a.s, st);
+  else kv8::launch_attn_d<64>(p, plan, a.s, st);
+  return cudaGetLastError();
+}
+
+}  // namespace thrift
