@@ -457,6 +457,11 @@ def kv8_alloc(num_pages: int, Hkv: int, page: int, d: int, device) -> Kv8Cache:
     return Kv8Cache(k, torch.empty_like(k), ks, torch.empty_like(ks))
 
 
+def _want_kv8(cache, name: str) -> None:
+    if not isinstance(cache, Kv8Cache):
+        raise TypeError(f"{name}: expected a Kv8Cache")
+
+
 def _kv8_tokens(x: torch.Tensor, name: str, heads: int, d: int, device) -> int:
     """Checks packed rows [n, heads, d] whose tokens may be strided; returns the token stride."""
     if not isinstance(x, torch.Tensor) or x.dim() != 3:
@@ -485,8 +490,6 @@ def _kv8_ints(t: torch.Tensor, name: str, shape, device) -> int:
 
 def _kv8_shape(cache: Kv8Cache, table, lens, cu, n, Hq, max_q, max_len, dtype):
     """The shape struct and the pointers of table, lens and cu."""
-    if not isinstance(cache, Kv8Cache):
-        raise TypeError("cache: expected a Kv8Cache")
     if not isinstance(table, torch.Tensor) or table.dim() != 2:
         raise ValueError("table: expected a [B, pages] tensor")
     B, cols = table.shape
@@ -518,6 +521,7 @@ def kv8_append(cache: Kv8Cache, k: torch.Tensor, v: torch.Tensor, table: torch.T
     the pages of their sequences.  table int32 [B, pages]; lens int32 [B], the new tokens included; cu int32
     [B + 1], sequence b's rows being cu[b] .. cu[b + 1] (None: one token each); max_q bounds a sequence's new
     tokens (default n, or 1 without cu)."""
+    _want_kv8(cache, "cache")
     ks = _kv8_tokens(k, "k", cache.Hkv, cache.d, cache.device)
     vs = _kv8_tokens(v, "v", cache.Hkv, cache.d, cache.device)
     if v.dtype is not k.dtype or v.shape != k.shape:
@@ -546,6 +550,7 @@ def kv8_attention(q: torch.Tensor, cache: Kv8Cache, table: torch.Tensor, lens: t
     window > 0 a query at position p sees t > p - window and the first `sinks` tokens.  table, lens, cu, max_q as
     for kv8_append; max_len bounds lens (default: what the table holds).  weights: fp32 [B, Hkv, >= max_len], to
     which each token's attention weights are added."""
+    _want_kv8(cache, "cache")
     qs = _kv8_tokens(q, "q", 0, cache.d, cache.device)
     n, Hq, d = q.shape
     shape, tp, lp, cp = _kv8_shape(cache, table, lens, cu, n, Hq, max_q, max_len, _KV8_DTYPES[q.dtype])
@@ -580,6 +585,7 @@ def kv8_attention_workspace(q: torch.Tensor, cache: Kv8Cache, table: torch.Tenso
                             max_len: Optional[int] = None, window: int = 0, sinks: int = 0,
                             weights: Optional[torch.Tensor] = None) -> int:
     """thrift_kv8_attn_workspace_bytes of a kv8_attention call with these arguments."""
+    _want_kv8(cache, "cache")
     _kv8_tokens(q, "q", 0, cache.d, cache.device)
     shape = _kv8_shape(cache, table, lens, cu, q.shape[0], q.shape[1], max_q, max_len, _KV8_DTYPES[q.dtype])[0]
     mask = Kv8Mask(window, sinks, 0.0)
@@ -594,9 +600,11 @@ def kv8_evict(cache: Kv8Cache, table: torch.Tensor, lens: torch.Tensor, weights:
     `sinks` and the last `recent` always among them) to the pages dst_table of dst -> (dst_lens int32 [B], kept
     int32 [B, Hkv, keep], the old positions, -1 past the last).  dst may be `cache` if its pages dst_table are
     none that the call reads; dst_weights must not overlap weights."""
+    _want_kv8(cache, "cache")
+    _want_kv8(dst, "dst")
     shape, tp, lp, _ = _kv8_shape(cache, table, lens, None, table.shape[0], cache.Hkv, 1, max_len, 0)
     dev, B, Hkv = cache.device, shape.B, cache.Hkv
-    if not isinstance(dst, Kv8Cache) or (dst.Hkv, dst.page, dst.d, dst.device) != (Hkv, cache.page, cache.d, dev):
+    if (dst.Hkv, dst.page, dst.d, dst.device) != (Hkv, cache.page, cache.d, dev):
         raise ValueError("dst: expected a Kv8Cache with the heads, page, d and device of cache")
     if not isinstance(dst_table, torch.Tensor) or dst_table.dim() != 2:
         raise ValueError("dst_table: expected a [B, pages] tensor")

@@ -541,7 +541,7 @@ static Plan make_plan(const thrift_kv8_shape& s, const thrift_kv8_mask& m, bool 
   const int R = 8 * p.nt;
   p.row_tiles = (int)((rows + R - 1) / R);
   long long span = s.max_len;
-  if (m.window > 0) {
+  if (m.window > 0 && m.window < s.max_len) {
     const long long w = (long long)m.window + (R + G - 1) / G + 2 * kTile + m.sinks + kTile;
     if (w < span) span = w;
   }
@@ -608,7 +608,10 @@ cudaError_t launch_kv8_attn(const Kv8Args& a, const Kv8Attn& t, cudaStream_t st)
   p.page_log2 = 31 - __builtin_clz((unsigned)a.s.page);
   p.table_cols = a.s.table_cols; p.n = a.s.n; p.max_q = a.s.max_q; p.max_len = a.s.max_len;
   p.num_pages = a.cache.num_pages;
-  p.window = t.mask.window; p.sinks = t.mask.sinks; p.fp16 = a.s.dtype == THRIFT_FP16;
+  // a window no sequence can outgrow hides nothing; the kernels' positions stay within 2^25
+  p.window = t.mask.window < a.s.max_len ? t.mask.window : 0;
+  p.sinks = t.mask.sinks < a.s.max_len ? t.mask.sinks : a.s.max_len;
+  p.fp16 = a.s.dtype == THRIFT_FP16;
   p.nsplit = plan.nsplit; p.chunk = plan.chunk; p.row_tiles = plan.row_tiles;
   const float scale = t.mask.softmax_scale > 0.0f ? t.mask.softmax_scale : 1.0f / sqrtf((float)a.s.d);
   p.scale_log2 = scale * kv8::kLog2e;
