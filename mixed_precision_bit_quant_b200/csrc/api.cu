@@ -422,10 +422,11 @@ thrift_status thrift_device_status(void* stream, uint32_t* detail) {
   if (read_and_clear_device_error(static_cast<cudaStream_t>(stream), &w) != cudaSuccess) return THRIFT_ERR_CUDA;
   if (read_and_clear_decode_error(&wd) != cudaSuccess) return THRIFT_ERR_CUDA;
   w |= wd << 8;
-  uint32_t wk = 0, wa = 0;
+  uint32_t wk = 0, wa = 0, wp = 0;
   if (read_and_clear_kv8_error(&wk) != cudaSuccess) return THRIFT_ERR_CUDA;
   if (read_and_clear_kv8_attn_error(&wa) != cudaSuccess) return THRIFT_ERR_CUDA;
-  w |= (wk | wa) << 16;
+  if (read_and_clear_kv8_prefill_error(&wp) != cudaSuccess) return THRIFT_ERR_CUDA;
+  w |= (wk | wa | wp) << 16;
   if (detail != nullptr) *detail = w;
   if ((w & ~0x10000u) != 0) return THRIFT_ERR_TIMEOUT;
   return w != 0 ? THRIFT_ERR_INVALID : THRIFT_OK;

@@ -98,6 +98,7 @@ cudaError_t launch_kv8_evict(const Kv8Args& a, const Kv8Evict& e, cudaStream_t s
 // bit 0: a bad length, range or page number; bit 1: a wait that ran out
 cudaError_t read_and_clear_kv8_error(uint32_t* word);
 cudaError_t read_and_clear_kv8_attn_error(uint32_t* word);
+cudaError_t read_and_clear_kv8_prefill_error(uint32_t* word);
 
 // Tensor-core rate probe (returns a thrift_status); cycles_dev: [ctas] per-CTA clock counts.
 int launch_mma_probe(int kind, int n, int iters, int ctas, float* ms, unsigned long long* cycles_dev,

@@ -11,7 +11,7 @@
 //                  state (maximum, sum, unnormalised output) when there are several runs
 //   merge_kernel   joins the runs' states of a row
 //   weights_kernel adds the rows' final weights to the running sums of the tokens
-#include "kv8.cuh"
+#include "kv8_attn.cuh"
 
 namespace thrift {
 namespace kv8 {
@@ -19,24 +19,6 @@ namespace kv8 {
 constexpr int kTile = 16;         // tokens of a warp's step (the m16 of its products)
 constexpr int kSplitThreads = 128;
 constexpr int kSplitWarps = kSplitThreads / 32;
-constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.69314718055994531f;
-
-struct AttnParams {
-  const uint8_t *k, *v, *ks, *vs;
-  const void* q;
-  long long q_stride;  // elements
-  const int32_t *table, *lens, *cu;
-  void* o;
-  float* lse;
-  float2* part_ml;  // [row][nsplit] maximum (log2 domain) and sum
-  float* part_o;    // [row][nsplit][D]
-  float* lse2;      // [row] log2-domain log-sum-exp for the weights (or null)
-  float* w;
-  long long w_cols;
-  int Hq, Hkv, G, page_log2, table_cols, n, max_q, max_len, num_pages, window, sinks, fp16;
-  int nsplit, chunk, row_tiles;  // chunk: 16-token tiles of a run
-  float scale_log2;
-};
 
 // D[16x8] += A[16x16] B[16x8], FP16 operands, FP32 accumulation.  Fragments (two FP16 per
 // register, the lower k in the low half; g = lane / 4, t = lane % 4): a0 (row g, k 2t, 2t+1),
@@ -53,43 +35,6 @@ __device__ __forceinline__ uint32_t movmatrix(uint32_t x) {
   uint32_t r;
   asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
   return r;
-}
-
-// The tokens that a tile of query rows can see, as an index space of 16-token tiles:
-// [0, s_tiles) are the sinks' tiles, the rest start at tile a_tile.
-struct Span {
-  int s_tiles, a_tile, count;
-  __device__ __forceinline__ int token(int v) const { return (v < s_tiles ? v : a_tile + (v - s_tiles)) * kTile; }
-};
-__device__ __forceinline__ Span visible_span(int p_lo, int p_hi, int window, int sinks) {
-  Span s{0, 0, 0};
-  if (p_hi < 0) return s;
-  if (window > 0) {
-    const int a = max(0, p_lo - window + 1) / kTile;
-    const int z = (min(sinks, p_hi + 1) + kTile - 1) / kTile;
-    if (a > z) {
-      s.s_tiles = z;
-      s.a_tile = a;
-    }
-  }
-  s.count = s.s_tiles + (p_hi + kTile) / kTile - s.a_tile;
-  return s;
-}
-
-// A row's log-sum-exp from its maximum (log2 domain) and sum.
-__device__ __forceinline__ void write_lse(const AttnParams& p, long long row, float m, float l) {
-  const float x = l > 0.0f ? m + log2f(l) : -INFINITY;
-  if (p.lse != nullptr) p.lse[row] = x * kLn2;
-  if (p.lse2 != nullptr) p.lse2[row] = x;
-}
-
-// Row r's packed index (token * Hq + head).
-__device__ __forceinline__ long long packed_row(const AttnParams& p, const Seq& s, int hk, int r) {
-  return (long long)(s.q0 + r / p.G) * p.Hq + hk * p.G + r % p.G;
-}
-__device__ __forceinline__ const uint32_t* query_row(const AttnParams& p, const Seq& s, int hk, int r, int d) {
-  const uint16_t* q = static_cast<const uint16_t*>(p.q) + (long long)(s.q0 + r / p.G) * p.q_stride + (hk * p.G + r % p.G) * d;
-  return reinterpret_cast<const uint32_t*>(q);
 }
 
 // Query row `r` as the FP16 B fragments of the logits' products, times 2^-e with
@@ -206,7 +151,7 @@ __global__ void __launch_bounds__(kSplitThreads) split_kernel(const AttnParams p
   if (rows <= 0) return;
   const int r_base = rt * R, r_cnt = min(rows, R);
   const int p_lo = s.pos0 + r_base / p.G, p_hi = s.pos0 + (r_base + r_cnt - 1) / p.G;
-  const Span span = visible_span(p_lo, p_hi, p.window, p.sinks);
+  const Span<kTile> span = visible_span<kTile>(p_lo, p_hi, p.window, p.sinks);
   const int v0 = split * p.chunk, v1 = min(span.count, v0 + p.chunk);
 
   extern __shared__ __align__(16) float sm[];
@@ -284,8 +229,7 @@ __global__ void __launch_bounds__(kSplitThreads) split_kernel(const AttnParams p
     for (int n = 0; n < NT; ++n)
 #pragma unroll
       for (int e = 0; e < 4; ++e) x[n][e] *= fs[n][e & 1] * kscale;
-    const bool full = tok + kTile - 1 <= p_lo && (p.window == 0 || tok > p_hi - p.window || tok + kTile <= p.sinks);
-    if (!full) {
+    if (!all_visible(p, tok, kTile, p_lo, p_hi)) {
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -528,30 +472,32 @@ __global__ void __launch_bounds__(128) weights_kernel(const AttnParams p) {
   }
 }
 
-// How a call is cut up: rows of a tile, runs per row tile.  The same for the workspace's
-// size and the launch.
-struct Plan {
-  int nt, row_tiles, nsplit, chunk;
-  size_t ml_off, o_off, lse_off, bytes;
-};
 static Plan make_plan(const thrift_kv8_shape& s, const thrift_kv8_mask& m, bool with_w) {
   Plan p;
   const long long G = s.Hq / s.Hkv, rows = (long long)s.max_q * G;
+  p.tiles128 = rows > 64;
   p.nt = rows <= 8 ? 1 : 2;
-  const int R = 8 * p.nt;
+  const int R = p.tiles128 ? kPrefillRows : 8 * p.nt, T = p.tiles128 ? kPrefillTile : kTile;
   p.row_tiles = (int)((rows + R - 1) / R);
+  // tokens that one row tile can see, rounded up to tiles at the sinks' and the window's ends
   long long span = s.max_len;
   if (m.window > 0 && m.window < s.max_len) {
-    const long long w = (long long)m.window + (R + G - 1) / G + 2 * kTile + m.sinks + kTile;
+    const long long w = (long long)m.window + (R + G - 1) / G + 2 * T + m.sinks + T;
     if (w < span) span = w;
   }
-  const long long tiles = (span + kTile - 1) / kTile + 1;
+  const long long tiles = (span + T - 1) / T + 1;
   const long long units = (long long)s.B * s.Hkv * p.row_tiles;
-  long long ns = (148 * 4) / units;
-  const long long most = (tiles + kSplitWarps - 1) / kSplitWarps;
-  ns = ns < 1 ? 1 : (ns > most ? most : ns);
-  if (ns > 64) ns = 64;
-  p.chunk = (int)(((tiles + ns - 1) / ns + kSplitWarps - 1) / kSplitWarps * kSplitWarps);
+  if (p.tiles128) {
+    const long long ns = 148 / units < 1 ? 1 : 148 / units;
+    p.chunk = (int)((tiles + ns - 1) / ns);
+    if (p.chunk < 2) p.chunk = 2;
+  } else {
+    long long ns = (148 * 4) / units;
+    const long long most = (tiles + kSplitWarps - 1) / kSplitWarps;
+    ns = ns < 1 ? 1 : (ns > most ? most : ns);
+    if (ns > 64) ns = 64;
+    p.chunk = (int)(((tiles + ns - 1) / ns + kSplitWarps - 1) / kSplitWarps * kSplitWarps);
+  }
   p.nsplit = (int)((tiles + p.chunk - 1) / p.chunk);
   const size_t nrow = (size_t)s.n * s.Hq;
   p.ml_off = 0;
@@ -568,20 +514,31 @@ static void launch_split(const AttnParams& p, dim3 grid, cudaStream_t s) {
 }
 
 template <int D>
-static void launch_attn_d(const AttnParams& p, const Plan& plan, const thrift_kv8_shape& s, cudaStream_t st) {
+static cudaError_t launch_attn_d(const AttnParams& p, const Plan& plan, const thrift_kv8_shape& s, cudaStream_t st) {
   const dim3 grid(plan.nsplit * plan.row_tiles, s.B * s.Hkv);
   int launches = 1;
-  if (plan.nt == 1) launch_split<D, 1>(p, grid, st);
-  else launch_split<D, 2>(p, grid, st);
+  if (plan.tiles128) {
+    const cudaError_t e = launch_prefill(p, s, st);
+    if (e != cudaSuccess) return e;
+  } else if (plan.nt == 1) {
+    launch_split<D, 1>(p, grid, st);
+  } else {
+    launch_split<D, 2>(p, grid, st);
+  }
   if (plan.nsplit > 1) {
     merge_kernel<D><<<dim3(s.max_q, s.B), 128, 0, st>>>(p);
     ++launches;
   }
-  if (p.w != nullptr) {
+  if (p.w != nullptr && plan.tiles128) {
+    const cudaError_t e = launch_tile_weights(p, s, st);
+    if (e != cudaSuccess) return e;
+    ++launches;
+  } else if (p.w != nullptr) {
     weights_kernel<D><<<dim3((s.max_len + 4 * kTile - 1) / (4 * kTile), s.B * s.Hkv), 128, 0, st>>>(p);
     ++launches;
   }
   count_launches(launches);
+  return cudaGetLastError();
 }
 
 }  // namespace kv8
@@ -615,9 +572,7 @@ cudaError_t launch_kv8_attn(const Kv8Args& a, const Kv8Attn& t, cudaStream_t st)
   p.nsplit = plan.nsplit; p.chunk = plan.chunk; p.row_tiles = plan.row_tiles;
   const float scale = t.mask.softmax_scale > 0.0f ? t.mask.softmax_scale : 1.0f / sqrtf((float)a.s.d);
   p.scale_log2 = scale * kv8::kLog2e;
-  if (a.s.d == 128) kv8::launch_attn_d<128>(p, plan, a.s, st);
-  else kv8::launch_attn_d<64>(p, plan, a.s, st);
-  return cudaGetLastError();
+  return a.s.d == 128 ? kv8::launch_attn_d<128>(p, plan, a.s, st) : kv8::launch_attn_d<64>(p, plan, a.s, st);
 }
 
 }  // namespace thrift

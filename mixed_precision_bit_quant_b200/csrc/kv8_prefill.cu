@@ -1,0 +1,753 @@
+// Attention over the paged 8-bit cache for many query rows (prompt chunks, verification of
+// several tokens): tcgen05 products on tiles of 128 query rows and 128 tokens.
+//
+// One CTA takes 256 rows of one kv head's group as two tiles of 128 and walks the visible
+// tokens in tiles of 128 (or a run of them, whose state merge_kernel joins).  16 warps:
+//   warps 0-3, 4-7  softmax of row tile 0 and 1: one thread owns one query row (= TMEM
+//              lane): S from TMEM, mask on edge tiles, running maximum, exponentials, P as
+//              FP16 back into S's columns; O is rescaled only when a row's maximum grew by 2^6
+//   warps 8-11 converters: a tile's K and V codes from global memory to FP16 in shared memory,
+//              each loaded while the tile before it is converted or waited for
+//   warp 12    tensor-memory allocator and issuer of S = Q K^T and O += P V; the row tiles
+//              alternate, so that one tile's products run under the other's exponentials
+// The products need one type for both operands: e4m3 codes are exact in FP16, with a
+// page's scale relative to the largest of the run (2^(e - e_ref), exact down to 2^-24, that is
+// for pages up to 2^21 smaller); the query enters as FP16 scaled by a power of two per row.
+#include "kv8_attn.cuh"
+
+namespace thrift {
+namespace kv8 {
+
+constexpr int kPfThreads = 512;
+constexpr int kPfSoftmaxRegs = 184, kPfConvRegs = 104, kPfOtherRegs = 40;
+static_assert(2 * kPfSoftmaxRegs + kPfConvRegs + kPfOtherRegs <= 512, "register split exceeds the launch budget");
+constexpr uint64_t kPfWaitNs = 2000000000ull;  // 2 s per wait: far above any legitimate wait
+constexpr int kUp = 6;          // codes enter FP16 times 2^6: at most 448 * 64 < 65504
+constexpr float kPfLazy = 6.0f;  // a row's maximum is raised when exceeded by 2^6
+constexpr float kPfShift = 9.0f; // P enters FP16 times 2^9: at most 2^15
+
+enum PfBar : int { KFULL = 0, KEMPTY = 2, VFULL = 4, VEMPTY = 6, SFULL = 8, PFULL = 10, PVDONE = 12, DRAIN = 14, NPFBAR = 15 };
+
+template <int D>
+struct PfLayout {
+  static constexpr int TILE = 128 * D * 2;  // FP16 tile: D/64 blocks of 128 rows x 128 bytes, 128-byte swizzle
+  static constexpr int OFF_Q = 0;             // two row tiles
+  static constexpr int OFF_K = 2 * TILE;      // two stages
+  static constexpr int OFF_V = 4 * TILE;      // two stages
+  static constexpr int OFF_BAR = 6 * TILE;
+  static constexpr int OFF_MISC = OFF_BAR + 8 * NPFBAR + 8;  // tmem holder, abort, bad page, e_ref of K, of V
+  static constexpr int BYTES = OFF_MISC + 32;
+  // at least 116 KB, so that one CTA (and its 512 TMEM columns) owns an SM
+  static constexpr int DYN = (BYTES + 1024 > 116 * 1024) ? BYTES + 1024 : 116 * 1024;
+  static constexpr uint32_t S_COL = 0, O_COL = 256;  // S of tile t at 128 t (P over its first half), O at 256 + D t
+};
+
+// kind::f16 with FP16 inputs, FP32 accumulation, M = 128; `mn_b`: B is N-major (its rows are k).
+__host__ __device__ constexpr uint32_t idesc_f16(int n, int mn_b) {
+  return (1u << 4) | ((uint32_t)mn_b << 16) | ((uint32_t)(n >> 3) << 17) | ((128u >> 4) << 24);
+}
+
+__device__ __forceinline__ void sts128(uint32_t addr, uint4 v) {
+  asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+
+__device__ __forceinline__ uint32_t hmul2_u32(uint32_t a, __half2 m) {
+  const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&a), m);
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+
+__device__ __forceinline__ void pf_raise(volatile int* abort) {
+  *abort = 1;
+  atomicOr(&g_error_word, 2u);
+}
+
+template <int D>
+__global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const AttnParams p) {
+  using L = PfLayout<D>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t sb = smem_u32(smem);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int bk = blockIdx.y, b = bk / p.Hkv, hk = bk % p.Hkv;
+  // the last rows of a prompt see the most tokens: they start first
+  const int split = blockIdx.x % p.nsplit, rt = p.row_tiles - 1 - blockIdx.x / p.nsplit;
+  const Seq s = load_seq(p.lens, p.cu, b, p.n, p.max_q, p.max_len);
+  if (s.bad && tid == 0 && blockIdx.x == 0 && hk == 0) raise_bad();
+  const int r_base = rt * kPrefillRows, r_cnt = min(s.nq * p.G - r_base, kPrefillRows);
+  if (r_cnt <= 0) return;
+  const int p_lo = s.pos0 + r_base / p.G, p_hi = s.pos0 + (r_base + r_cnt - 1) / p.G;
+  const Span<kPrefillTile> span = visible_span<kPrefillTile>(p_lo, p_hi, p.window, p.sinks);
+  const int v0 = split * p.chunk, nj = min(span.count, v0 + p.chunk) - v0;
+  if (nj <= 0) {  // nothing in this run: an empty state, or rows that see nothing
+    for (int r = tid; r < r_cnt; r += kPfThreads) {
+      const long long row = packed_row(p, s, hk, r_base + r);
+      if (p.nsplit > 1) {
+        p.part_ml[row * p.nsplit + split] = make_float2(-INFINITY, 0.0f);
+      } else {
+        write_lse(p, row, -INFINITY, 0.0f);
+        for (int c = 0; c < D / 8; ++c) reinterpret_cast<uint4*>(p.o)[row * (D / 8) + c] = make_uint4(0, 0, 0, 0);
+      }
+    }
+    return;
+  }
+  const int ntile = r_cnt > 128 ? 2 : 1;
+
+  auto BAR = [&](int k) -> uint32_t { return sb + L::OFF_BAR + 8 * k; };
+  volatile uint32_t* misc = reinterpret_cast<volatile uint32_t*>(smem + L::OFF_MISC);
+  volatile int* abort = reinterpret_cast<volatile int*>(smem + L::OFF_MISC + 4);
+  int* eref = reinterpret_cast<int*>(smem + L::OFF_MISC + 12);
+  if (tid == 0) {
+    for (int k = 0; k < NPFBAR; ++k)
+      mbar_init(BAR(k), (k >= KFULL && k < KFULL + 2) || (k >= VFULL && k < VFULL + 2) || (k >= PFULL && k < PFULL + 2) ? 4 : 1);
+    *abort = 0;
+    misc[2] = 0;
+    eref[0] = eref[1] = 0;
+    fence_mbar_init();
+  }
+  if (warp == 12) {
+    tmem_alloc(smem_u32(smem + L::OFF_MISC), 512);
+    tmem_relinquish();
+  }
+  __syncthreads();
+  const int32_t* trow = p.table + (long long)b * p.table_cols;
+  const int page_tok = 1 << p.page_log2;
+  // the largest exponents of the run's pages, and whether one is not of the pool
+  {
+    int ek = 0, ev = 0;
+    bool bad = false;
+    const int per = page_tok < kPrefillTile ? kPrefillTile >> p.page_log2 : 1;  // pages of a tile
+    for (int i = tid; i < nj * per; i += kPfThreads) {
+      const int tok = span.token(v0 + i / per) + (i % per) * page_tok;
+      if (!any_visible(p, tok, page_tok, p_lo, p_hi)) continue;
+      const int pg = __ldg(trow + (tok >> p.page_log2));
+      if (pg < 0 || pg >= p.num_pages) {
+        bad = true;
+        continue;
+      }
+      ek = max(ek, (int)__ldg(p.ks + (long long)pg * p.Hkv + hk));
+      ev = max(ev, (int)__ldg(p.vs + (long long)pg * p.Hkv + hk));
+    }
+    ek = __reduce_max_sync(0xffffffffu, ek);
+    ev = __reduce_max_sync(0xffffffffu, ev);
+    if (lane == 0) {
+      atomicMax(eref, ek);
+      atomicMax(eref + 1, ev);
+    }
+    if (bad) {
+      misc[2] = 1;
+      raise_bad();
+    }
+  }
+  // a softmax thread's query row: FP16, scaled by a power of two, to shared memory
+  float qscale = 0.0f;
+  const int tile = warp >> 2;  // of a softmax warp
+  const int row = (warp & 3) * 32 + lane;
+  if (warp < 8 && tile < ntile) {
+    const int r = tile * 128 + row;
+    uint32_t q[D / 2];
+#pragma unroll
+    for (int c = 0; c < D / 8; ++c) {
+      uint4 u = make_uint4(0, 0, 0, 0);
+      if (r < r_cnt) u = __ldg(reinterpret_cast<const uint4*>(query_row(p, s, hk, r_base + r, D)) + c);
+      q[4 * c] = u.x; q[4 * c + 1] = u.y; q[4 * c + 2] = u.z; q[4 * c + 3] = u.w;
+    }
+    uint32_t am = 0;
+#pragma unroll
+    for (int c = 0; c < D / 2; ++c) am = __vmaxu2(am, q[c] & 0x7FFF7FFFu);
+    am = max(am & 0xFFFFu, am >> 16);
+    const int e = max(-100, (int)(__float_as_uint(pair_to_float2(am, p.fp16).x) >> 23) - 127 - 14);
+    const float down = pow2f(-e);
+    qscale = pow2f(e) * p.scale_log2;
+#pragma unroll
+    for (int c = 0; c < D / 8; ++c) {
+      uint32_t h[4];
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        const float2 f = pair_to_float2(q[4 * c + x], p.fp16);
+        const __half2 hh = __floats2half2_rn(f.x * down, f.y * down);
+        h[x] = *reinterpret_cast<const uint32_t*>(&hh);
+      }
+      sts128(sb + L::OFF_Q + tile * L::TILE + (c >> 3) * 16384 + row * 128 + (((c & 7) ^ (row & 7)) << 4),
+             make_uint4(h[0], h[1], h[2], h[3]));
+    }
+    fence_proxy_async_smem();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = misc[0];
+  const int kref = eref[0], vref = eref[1];
+  volatile int never = 0;
+
+  if (warp >= 12) {
+    regs_dec<kPfOtherRegs>();
+    if (warp == 12 && lane == 0) {
+      // ------------------------------------------------------------ issuer
+      bool ok = true;
+      auto qk = [&](int t, int st) {
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+          const uint32_t off = (k >> 2) * 16384 + (k & 3) * 32;
+          mma_bf16_ss(tmem + L::S_COL + 128 * t, smem_desc(sb + L::OFF_Q + t * L::TILE + off, 16, 1024, SWZ_128B),
+                      smem_desc(sb + L::OFF_K + st * L::TILE + off, 16, 1024, SWZ_128B), idesc_f16(128, 0), k > 0);
+        }
+        tc_commit(BAR(SFULL + t));
+      };
+      ok = mbar_wait(BAR(KFULL), 0, abort, kPfWaitNs);
+      if (ok) {
+        tc_fence_after();
+        for (int t = 0; t < ntile; ++t) qk(t, 0);
+        tc_commit(BAR(KEMPTY));
+      }
+      for (int j = 0; ok && j < nj; ++j) {
+        const int st = j & 1, sn = st ^ 1;
+        for (int t = 0; t < ntile; ++t) {
+          if (!mbar_wait(BAR(PFULL + t), j & 1, abort, kPfWaitNs) ||
+              (t == 0 && !mbar_wait(BAR(VFULL + st), (j >> 1) & 1, abort, kPfWaitNs))) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+#pragma unroll
+          for (int k = 0; k < 8; ++k)  // 16 tokens a step: 16 rows of 128 bytes
+            mma_bf16_ts(tmem + L::O_COL + D * t, tmem + L::S_COL + 128 * t + 8 * k,
+                        smem_desc(sb + L::OFF_V + st * L::TILE + 2048 * k, 16384, 1024, SWZ_128B), idesc_f16(D, 1),
+                        (j > 0 || k > 0) ? 1u : 0u);
+          tc_commit(BAR(PVDONE + t));
+          if (j + 1 < nj) {
+            if (t == 0 && !mbar_wait(BAR(KFULL + sn), ((j + 1) >> 1) & 1, abort, kPfWaitNs)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            qk(t, sn);
+          }
+        }
+        tc_commit(BAR(VEMPTY + st));
+        if (j + 1 < nj) tc_commit(BAR(KEMPTY + sn));
+      }
+      if (!ok) pf_raise(abort);
+      tc_commit(BAR(DRAIN));  // every product issued above completes before TMEM is released
+      mbar_wait(BAR(DRAIN), 0, &never, kPfWaitNs);
+    }
+  } else if (warp >= 8) {
+    regs_dec<kPfConvRegs>();
+    // -------------------------------------------------------------- converters
+    constexpr int LPR = D / 16, RPI = 32 / LPR;  // lanes per token, tokens per load of a warp
+    const int cw = warp - 8, c = lane % LPR, rr = lane / LPR;
+    // lane l of a batch: tile l / 2, group of 16 tokens 2 cw + (l & 1) of it
+    int l_page = -1, l_ks = 0, l_vs = 0;
+    auto batch = [&](int j0) {
+      const int j = j0 + (lane >> 1);
+      l_page = -1;
+      if (j < nj) {
+        const int tok = span.token(v0 + j) + 32 * cw + 16 * (lane & 1);
+        if (any_visible(p, tok, 16, p_lo, p_hi)) {
+          const int pg = __ldg(trow + (tok >> p.page_log2));
+          if (pg >= 0 && pg < p.num_pages) {
+            l_page = pg;
+            l_ks = __ldg(p.ks + (long long)pg * p.Hkv + hk);
+            l_vs = __ldg(p.vs + (long long)pg * p.Hkv + hk);
+          }
+        }
+      }
+    };
+    auto load = [&](const uint8_t* base, int j, uint4 (&u)[LPR]) {
+      const int tok = span.token(v0 + j) + 32 * cw;
+#pragma unroll
+      for (int i = 0; i < LPR; ++i) {
+        const int grp = i * RPI / 16;
+        const int pg = __shfl_sync(0xffffffffu, l_page, 2 * (j & 15) + grp);
+        u[i] = make_uint4(0, 0, 0, 0);
+        if (pg >= 0) {
+          const int slot = (tok + i * RPI + rr) & (page_tok - 1);
+          u[i] = __ldg(reinterpret_cast<const uint4*>(base + ((((long long)pg * p.Hkv + hk) << p.page_log2) + slot) * D) + c);
+        }
+      }
+    };
+    // the loaded rows as FP16 into a tile; `edge`: rows that no query row sees become zero
+    auto store = [&](uint32_t dst, uint4 (&u)[LPR], const __half2 (&m)[2], bool edge, int tok) {
+#pragma unroll
+      for (int i = 0; i < LPR; ++i) {
+        const int r = 32 * cw + i * RPI + rr;
+        if (edge && !any_visible(p, tok + r, 1, p_lo, p_hi)) u[i] = make_uint4(0, 0, 0, 0);
+        const __half2 f = m[i * RPI / 16];
+        const uint4 lo = make_uint4(hmul2_u32(e4m3x2_to_h2(u[i].x & 0xFFFFu), f), hmul2_u32(e4m3x2_to_h2(u[i].x >> 16), f),
+                                    hmul2_u32(e4m3x2_to_h2(u[i].y & 0xFFFFu), f), hmul2_u32(e4m3x2_to_h2(u[i].y >> 16), f));
+        const uint4 hi = make_uint4(hmul2_u32(e4m3x2_to_h2(u[i].z & 0xFFFFu), f), hmul2_u32(e4m3x2_to_h2(u[i].z >> 16), f),
+                                    hmul2_u32(e4m3x2_to_h2(u[i].w & 0xFFFFu), f), hmul2_u32(e4m3x2_to_h2(u[i].w >> 16), f));
+        // chunks 2c and 2c + 1 of the row; the row's second half writes them in the other
+        // order, so that eight lanes' stores meet all banks
+        const int ch = 2 * c, blk = ch >> 3, x0 = (ch & 7), sw = (c >> 2) & 1;
+        const uint32_t rowa = dst + blk * 16384 + r * 128;
+        sts128(rowa + (((x0 + sw) ^ (r & 7)) << 4), sw ? hi : lo);
+        sts128(rowa + (((x0 + 1 - sw) ^ (r & 7)) << 4), sw ? lo : hi);
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+    };
+    auto factors = [&](int j, int code, int ref, __half2 (&m)[2]) {
+#pragma unroll
+      for (int g = 0; g < 2; ++g) {
+        const int e = __shfl_sync(0xffffffffu, code, 2 * (j & 15) + g);
+        m[g] = __float2half2_rn(pow2f(max(-24, e - ref + kUp)));
+      }
+    };
+    bool ok = true;
+    uint4 uk[LPR], uv[LPR];
+    batch(0);
+    load(p.k, 0, uk);
+    load(p.v, 0, uv);
+    for (int j = 0; j < nj; ++j) {
+      const int st = j & 1, use = j >> 1, tok = span.token(v0 + j);
+      const bool edge = !all_visible(p, tok, kPrefillTile, p_lo, p_hi);
+      __half2 mk[2], mv[2];
+      factors(j, l_ks, kref, mk);
+      factors(j, l_vs, vref, mv);
+      if (use > 0 && !__all_sync(0xffffffffu, mbar_wait(BAR(KEMPTY + st), (use - 1) & 1, abort, kPfWaitNs))) { ok = false; break; }
+      store(sb + L::OFF_K + st * L::TILE, uk, mk, edge, tok);
+      if (lane == 0) mbar_arrive(BAR(KFULL + st));
+      if (j + 1 < nj) {
+        if (((j + 1) & 15) == 0) batch(j + 1);
+        load(p.k, j + 1, uk);
+      }
+      if (use > 0 && !__all_sync(0xffffffffu, mbar_wait(BAR(VEMPTY + st), (use - 1) & 1, abort, kPfWaitNs))) { ok = false; break; }
+      store(sb + L::OFF_V + st * L::TILE, uv, mv, edge, tok);
+      if (lane == 0) mbar_arrive(BAR(VFULL + st));
+      if (j + 1 < nj) load(p.v, j + 1, uv);
+    }
+    if (!ok && lane == 0) pf_raise(abort);
+  } else {
+    regs_inc<kPfSoftmaxRegs>();
+    // -------------------------------------------------------------- softmax
+    if (tile < ntile) {
+      const int r = tile * 128 + row;  // row of the CTA
+      const int pos = r < r_cnt ? s.pos0 + (r_base + r) / p.G : -1;
+      const int t_lo = s.pos0 + (r_base + tile * 128) / p.G;
+      const int t_hi = s.pos0 + (r_base + min(r_cnt, tile * 128 + 128) - 1) / p.G;
+      const float sc = qscale * pow2f(max(-126, kref - 127 - kUp));
+      const bool bad_pages = misc[2] != 0;
+      const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+      const uint32_t s_addr = lane_base + L::S_COL + 128 * tile, o_addr = lane_base + L::O_COL + D * tile;
+      float m_ref = -INFINITY, l = 0.0f;
+      bool ok = true;
+      for (int j = 0; j < nj; ++j) {
+        if (!__all_sync(0xffffffffu, mbar_wait(BAR(SFULL + tile), j & 1, abort, kPfWaitNs))) { ok = false; break; }
+        tc_fence_after();
+        uint32_t v[128];
+#pragma unroll
+        for (int c4 = 0; c4 < 4; ++c4) tmem_ld32(s_addr + 32 * c4, *reinterpret_cast<uint32_t(*)[32]>(&v[32 * c4]));
+        tmem_ld_wait();
+        const int tok = span.token(v0 + j);
+        if (bad_pages || !all_visible(p, tok, kPrefillTile, t_lo, t_hi)) {
+          // columns [lo, hi] are in sight, and those below `sk`
+          const int hi = pos - tok, lo = p.window > 0 ? pos - p.window + 1 - tok : 0;
+          const int sk = min(p.sinks - tok, hi + 1);
+#pragma unroll
+          for (int c = 0; c < 128; ++c)
+            if (!((c >= lo && c <= hi) || (p.window > 0 && c < sk))) v[c] = __float_as_uint(-INFINITY);
+          if (bad_pages) {
+            for (int g = 0; g < 8; ++g) {
+              const int tg = tok + 16 * g;
+              bool gone = false;
+              if (any_visible(p, tg, 16, p_lo, p_hi)) {
+                const int pg = __ldg(trow + (tg >> p.page_log2));
+                gone = pg < 0 || pg >= p.num_pages;
+              }
+              if (gone) {
+#pragma unroll
+                for (int c = 0; c < 128; ++c)
+                  if ((c >> 4) == g) v[c] = __float_as_uint(-INFINITY);
+              }
+            }
+          }
+        }
+        float mloc;
+        {
+          float t1[43];
+#pragma unroll
+          for (int c = 0; c < 42; ++c)
+            t1[c] = fmax3(__uint_as_float(v[3 * c]), __uint_as_float(v[3 * c + 1]), __uint_as_float(v[3 * c + 2]));
+          t1[42] = fmaxf(__uint_as_float(v[126]), __uint_as_float(v[127]));
+          float t2[15];
+#pragma unroll
+          for (int c = 0; c < 14; ++c) t2[c] = fmax3(t1[3 * c], t1[3 * c + 1], t1[3 * c + 2]);
+          t2[14] = t1[42];
+          float t3[5];
+#pragma unroll
+          for (int c = 0; c < 5; ++c) t3[c] = fmax3(t2[3 * c], t2[3 * c + 1], t2[3 * c + 2]);
+          mloc = fmaxf(fmax3(t3[0], t3[1], t3[2]), fmaxf(t3[3], t3[4])) * sc;
+        }
+        float alpha = 1.0f;
+        const bool grow = mloc > m_ref + kPfLazy;
+        if (__any_sync(0xffffffffu, grow)) {
+          const float m_new = fmaxf(m_ref, mloc);
+          alpha = m_ref == -INFINITY ? 0.0f : ex2_approx(m_ref - m_new);
+          m_ref = m_new;
+          l *= alpha;
+          if (j > 0) {
+            if (!__all_sync(0xffffffffu, mbar_wait(BAR(PVDONE + tile), (j - 1) & 1, abort, kPfWaitNs))) { ok = false; break; }
+            tc_fence_after();
+#pragma unroll
+            for (int c4 = 0; c4 < D / 16; ++c4) {  // 16 columns at a time: S's 128 registers are live
+              uint32_t o[16];
+              tmem_ld16(o_addr + 16 * c4, o);
+              tmem_ld_wait();
+#pragma unroll
+              for (int c = 0; c < 16; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * alpha);
+              tmem_st16(o_addr + 16 * c4, o);
+            }
+          }
+        }
+        const float nb = m_ref == -INFINITY ? 0.0f : kPfShift - m_ref;
+        const uint64_t sc2 = f2pack(sc, sc), nb2 = f2pack(nb, nb);
+        uint64_t acc[4] = {0, 0, 0, 0};
+#pragma unroll
+        for (int ch = 0; ch < 4; ++ch) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int t = 0; t < 16; ++t) {
+            const int i = 16 * ch + t;
+            const uint64_t y = ffma2(f2pack(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])), sc2, nb2);
+            float a0, a1;
+            f2unpack(y, a0, a1);
+            a0 = ex2_approx(a0);
+            a1 = ex2_approx(a1);
+            acc[t & 3] = fadd2(acc[t & 3], f2pack(a0, a1));
+            const __half2 h = __floats2half2_rn(a0, a1);
+            pk[t] = *reinterpret_cast<const uint32_t*>(&h);
+          }
+          tmem_st16(s_addr + 16 * ch, pk);
+        }
+        float x0, x1, x2, x3;
+        f2unpack(fadd2(acc[0], acc[1]), x0, x1);
+        f2unpack(fadd2(acc[2], acc[3]), x2, x3);
+        l += (x0 + x1) + (x2 + x3);
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(BAR(PFULL + tile));
+      }
+      ok = ok && __all_sync(0xffffffffu, mbar_wait(BAR(PVDONE + tile), (nj - 1) & 1, abort, kPfWaitNs));
+      if (!ok) {
+        if (lane == 0) pf_raise(abort);
+      } else {
+        tc_fence_after();
+        const long long prow = r < r_cnt ? packed_row(p, s, hk, r_base + r) : 0;
+        // codes' units back to values: 2^(e_ref - 6), in two steps (e_ref may be -127)
+        const float back = scale_value((uint32_t)vref), down = 1.0f / (1 << kUp);
+        const float f = p.nsplit > 1 ? down : (l > 0.0f ? down / l : 0.0f);
+#pragma unroll
+        for (int c4 = 0; c4 < D / 32; ++c4) {
+          uint32_t o[32];
+          tmem_ld32(o_addr + 32 * c4, o);
+          tmem_ld_wait();
+#pragma unroll
+          for (int c = 0; c < 32; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * f * back);
+          if (r < r_cnt) {
+            if (p.nsplit > 1) {
+              uint4* dst = reinterpret_cast<uint4*>(p.part_o + (prow * p.nsplit + split) * D + 32 * c4);
+#pragma unroll
+              for (int c = 0; c < 8; ++c) dst[c] = make_uint4(o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]);
+            } else {
+              uint4* dst = reinterpret_cast<uint4*>(p.o) + prow * (D / 8) + 4 * c4;
+#pragma unroll
+              for (int c = 0; c < 4; ++c) {
+                uint32_t w[4];
+#pragma unroll
+                for (int x = 0; x < 4; ++x)
+                  w[x] = float2_to_pair(__uint_as_float(o[8 * c + 2 * x]), __uint_as_float(o[8 * c + 2 * x + 1]), p.fp16);
+                dst[c] = make_uint4(w[0], w[1], w[2], w[3]);
+              }
+            }
+          }
+        }
+        if (r < r_cnt) {
+          if (p.nsplit > 1) p.part_ml[prow * p.nsplit + split] = make_float2(l > 0.0f ? m_ref - kPfShift : -INFINITY, l);
+          else write_lse(p, prow, m_ref - kPfShift, l);
+        }
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 12) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// The weight sums of many rows: w[t] += sum over rows exp(s - lse).
+//
+// One CTA takes 128 tokens of a sequence and kv head and walks the tiles of 128 query rows
+// that see them: S^T = K Q^T puts a token on a TMEM lane, so a token's sum over rows
+// is a thread's sum over columns -- no exchange, and in a fixed order.
+//   warps 0-3, 4-7  the even and the odd row tiles' exponentials and sums
+//   warps 8-11 query rows to FP16 in shared memory (one thread a row), with the row's
+//              scale and log-sum-exp
+//   warp 12    tensor-memory allocator and issuer
+// ---------------------------------------------------------------------------
+enum TwBar : int { QFULL = 0, QEMPTY = 3, WFULL = 6, WEMPTY = 8, WDRAIN = 10, NTWBAR = 11 };
+constexpr int kTwStages = 3, kTwThreads = 416;
+
+template <int D>
+struct TwLayout {
+  static constexpr int TILE = 128 * D * 2;
+  static constexpr int OFF_K = 0;
+  static constexpr int OFF_Q = TILE;                        // kTwStages row tiles
+  static constexpr int OFF_ROW = OFF_Q + kTwStages * TILE;  // [stage][64] of two rows' scale, scale, -lse, -lse
+  static constexpr int OFF_SUM = OFF_ROW + kTwStages * 1024;  // [128] the odd tiles' sums
+  static constexpr int OFF_BAR = OFF_SUM + 512;
+  static constexpr int OFF_MISC = OFF_BAR + 8 * NTWBAR + 8;
+  static constexpr int DYN = OFF_MISC + 32 + 1024;
+};
+
+template <int D>
+__global__ void __launch_bounds__(kTwThreads, 1) tile_weights_kernel(const AttnParams p) {
+  using L = TwLayout<D>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t sb = smem_u32(smem);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int bk = blockIdx.y, b = bk / p.Hkv, hk = bk % p.Hkv;
+  const Seq s = load_seq(p.lens, p.cu, b, p.n, p.max_q, p.max_len);
+  const int t0 = blockIdx.x * 128;
+  // the rows that see some of the tokens, in whole tiles
+  const int i0 = max(0, t0 - s.pos0);
+  int i1 = s.nq;
+  if (p.window > 0 && t0 >= p.sinks) i1 = min(i1, t0 + 127 + p.window - s.pos0);
+  if (t0 >= s.len || i0 >= i1) return;
+  const int rows = s.nq * p.G, rt0 = i0 * p.G / 128, nt = (i1 * p.G + 127) / 128 - rt0;
+
+  auto BAR = [&](int k) -> uint32_t { return sb + L::OFF_BAR + 8 * k; };
+  volatile uint32_t* misc = reinterpret_cast<volatile uint32_t*>(smem + L::OFF_MISC);
+  volatile int* abort = reinterpret_cast<volatile int*>(smem + L::OFF_MISC + 4);
+  int* eref = reinterpret_cast<int*>(smem + L::OFF_MISC + 8);
+  if (tid == 0) {
+    // a stage is free once its product completed and the four warps that read its rows' numbers did
+    for (int k = 0; k < NTWBAR; ++k)
+      mbar_init(BAR(k), k < QEMPTY ? 4 : k < WFULL ? 5 : (k >= WEMPTY && k < WDRAIN) ? 4 : 1);
+    *abort = 0;
+    *eref = 0;
+    fence_mbar_init();
+  }
+  if (warp == 12) {
+    tmem_alloc(smem_u32(smem + L::OFF_MISC), 256);
+    tmem_relinquish();
+  }
+  __syncthreads();
+  const int32_t* trow = p.table + (long long)b * p.table_cols;
+  // K's codes as FP16, each page relative to the largest exponent of the tile's pages
+  constexpr int VR = D / 16, ITEMS = 128 * VR / 256;
+  uint4 u[ITEMS];
+  int ks[ITEMS];
+  if (warp < 8) {
+    int top = 0;
+#pragma unroll
+    for (int i = 0; i < ITEMS; ++i) {
+      const int it = tid + 256 * i, tok = t0 + it / VR;
+      u[i] = make_uint4(0, 0, 0, 0);
+      ks[i] = 0;
+      if (tok < s.len) {
+        const int pg = __ldg(trow + (tok >> p.page_log2));
+        if (pg >= 0 && pg < p.num_pages) {
+          const long long ph = (long long)pg * p.Hkv + hk;
+          ks[i] = __ldg(p.ks + ph);
+          u[i] = __ldg(reinterpret_cast<const uint4*>(p.k + ((ph << p.page_log2) + (tok & ((1 << p.page_log2) - 1))) * D) + it % VR);
+        }
+      }
+      top = max(top, ks[i]);
+    }
+    top = __reduce_max_sync(0xffffffffu, top);
+    if (lane == 0) atomicMax(eref, top);
+  }
+  __syncthreads();
+  const int kref = *eref;
+  if (warp < 8) {
+#pragma unroll
+    for (int i = 0; i < ITEMS; ++i) {
+      const int it = tid + 256 * i, r = it / VR, ch = 2 * (it % VR);
+      const __half2 f = __float2half2_rn(pow2f(max(-24, ks[i] - kref + kUp)));
+      const uint32_t rowa = sb + L::OFF_K + (ch >> 3) * 16384 + r * 128;
+      sts128(rowa + (((ch & 7) ^ (r & 7)) << 4),
+             make_uint4(hmul2_u32(e4m3x2_to_h2(u[i].x & 0xFFFFu), f), hmul2_u32(e4m3x2_to_h2(u[i].x >> 16), f),
+                        hmul2_u32(e4m3x2_to_h2(u[i].y & 0xFFFFu), f), hmul2_u32(e4m3x2_to_h2(u[i].y >> 16), f)));
+      sts128(rowa + ((((ch & 7) + 1) ^ (r & 7)) << 4),
+             make_uint4(hmul2_u32(e4m3x2_to_h2(u[i].z & 0xFFFFu), f), hmul2_u32(e4m3x2_to_h2(u[i].z >> 16), f),
+                        hmul2_u32(e4m3x2_to_h2(u[i].w & 0xFFFFu), f), hmul2_u32(e4m3x2_to_h2(u[i].w >> 16), f)));
+    }
+    fence_proxy_async_smem();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = misc[0];
+  volatile int never = 0;
+  float sum = 0.0f;
+  bool ok = true;
+
+  if (warp == 12) {
+    if (lane == 0) {
+      for (int j = 0; j < nt; ++j) {
+        const int st = j % kTwStages, buf = j & 1;
+        if (!mbar_wait(BAR(QFULL + st), (j / kTwStages) & 1, abort, kPfWaitNs) ||
+            (j >= 2 && !mbar_wait(BAR(WEMPTY + buf), ((j >> 1) - 1) & 1, abort, kPfWaitNs))) {
+          pf_raise(abort);
+          break;
+        }
+        tc_fence_after();
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+          const uint32_t off = (k >> 2) * 16384 + (k & 3) * 32;
+          mma_bf16_ss(tmem + 128 * buf, smem_desc(sb + L::OFF_K + off, 16, 1024, SWZ_128B),
+                      smem_desc(sb + L::OFF_Q + st * L::TILE + off, 16, 1024, SWZ_128B), idesc_f16(128, 0), k > 0);
+        }
+        tc_commit(BAR(QEMPTY + st));
+        tc_commit(BAR(WFULL + buf));
+      }
+      tc_commit(BAR(WDRAIN));
+      mbar_wait(BAR(WDRAIN), 0, &never, kPfWaitNs);
+    }
+  } else if (warp >= 8) {
+    const int row = (warp - 8) * 32 + lane;
+    const float kf = pow2f(max(-126, kref - 127 - kUp)) * p.scale_log2;
+    for (int j = 0; j < nt; ++j) {
+      const int st = j % kTwStages, r = (rt0 + j) * 128 + row;
+      uint32_t q[D / 2];
+#pragma unroll
+      for (int c = 0; c < D / 8; ++c) {
+        uint4 x = make_uint4(0, 0, 0, 0);
+        if (r < rows) x = __ldg(reinterpret_cast<const uint4*>(query_row(p, s, hk, r, D)) + c);
+        q[4 * c] = x.x; q[4 * c + 1] = x.y; q[4 * c + 2] = x.z; q[4 * c + 3] = x.w;
+      }
+      const float lse2 = r < rows ? p.lse2[packed_row(p, s, hk, r)] : -INFINITY;
+      uint32_t am = 0;
+#pragma unroll
+      for (int c = 0; c < D / 2; ++c) am = __vmaxu2(am, q[c] & 0x7FFF7FFFu);
+      am = max(am & 0xFFFFu, am >> 16);
+      const int e = max(-100, (int)(__float_as_uint(pair_to_float2(am, p.fp16).x) >> 23) - 127 - 14);
+      const float down = pow2f(-e);
+      if (j >= kTwStages && !__all_sync(0xffffffffu, mbar_wait(BAR(QEMPTY + st), (j / kTwStages - 1) & 1, abort, kPfWaitNs))) {
+        ok = false;
+        break;
+      }
+#pragma unroll
+      for (int c = 0; c < D / 8; ++c) {
+        uint32_t h[4];
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const float2 f = pair_to_float2(q[4 * c + x], p.fp16);
+          const __half2 hh = __floats2half2_rn(f.x * down, f.y * down);
+          h[x] = *reinterpret_cast<const uint32_t*>(&hh);
+        }
+        sts128(sb + L::OFF_Q + st * L::TILE + (c >> 3) * 16384 + row * 128 + (((c & 7) ^ (row & 7)) << 4),
+               make_uint4(h[0], h[1], h[2], h[3]));
+      }
+      // a row that sees nothing (lse = -inf) or is none gets -inf: its exponentials are 0
+      float* rp = reinterpret_cast<float*>(smem + L::OFF_ROW + st * 1024) + 4 * (row >> 1) + (row & 1);
+      rp[0] = pow2f(e) * kf;
+      rp[2] = lse2 == -INFINITY ? -INFINITY : -lse2;
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(BAR(QFULL + st));
+    }
+    if (!ok && lane == 0) pf_raise(abort);
+  } else {
+    const int grp = warp >> 2, tok = t0 + (warp & 3) * 32 + lane;
+    const uint32_t base = tmem + ((uint32_t)((warp & 3) * 32) << 16) + 128 * grp;
+    uint64_t acc[2] = {0, 0};
+    for (int j = grp; j < nt; j += 2) {
+      const int st = j % kTwStages;
+      // the rows' numbers are written before QFULL, which the product waited for
+      if (!__all_sync(0xffffffffu, mbar_wait(BAR(WFULL + grp), (j >> 1) & 1, abort, kPfWaitNs) &&
+                                       mbar_wait(BAR(QFULL + st), (j / kTwStages) & 1, abort, kPfWaitNs))) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      const float4* rp = reinterpret_cast<const float4*>(smem + L::OFF_ROW + st * 1024);
+      const int r0 = (rt0 + j) * 128;
+      const bool edge = !all_visible(p, t0, 128, s.pos0 + r0 / p.G, s.pos0 + (min(rows, r0 + 128) - 1) / p.G);
+#pragma unroll
+      for (int c4 = 0; c4 < 4; ++c4) {
+        uint32_t v[32];
+        tmem_ld32(base + 32 * c4, v);
+        tmem_ld_wait();
+        if (c4 == 3) {  // S is read: its buffer may take the next product
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(BAR(WEMPTY + grp));
+        }
+        if (edge) {
+#pragma unroll
+          for (int c = 0; c < 32; ++c) {
+            const int pos = s.pos0 + (r0 + 32 * c4 + c) / p.G;
+            const bool see = tok <= pos && (p.window == 0 || tok > pos - p.window || tok < p.sinks);
+            if (!see) v[c] = __float_as_uint(-INFINITY);
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const float4 f = rp[16 * c4 + i];
+          const uint64_t y = ffma2(f2pack(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])), f2pack(f.x, f.y), f2pack(f.z, f.w));
+          float a0, a1;
+          f2unpack(y, a0, a1);
+          acc[i & 1] = fadd2(acc[i & 1], f2pack(ex2_approx(a0), ex2_approx(a1)));
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(BAR(QEMPTY + st));
+    }
+    if (!ok && lane == 0) pf_raise(abort);
+    float a0, a1;
+    f2unpack(fadd2(acc[0], acc[1]), a0, a1);
+    sum = a0 + a1;
+    if (grp == 1) reinterpret_cast<float*>(smem + L::OFF_SUM)[tok - t0] = sum;
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 12) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 256);
+  }
+  if (tid < 128 && t0 + tid < s.len) {
+    const int pg = __ldg(trow + ((t0 + tid) >> p.page_log2));
+    if (pg >= 0 && pg < p.num_pages) {
+      float* w = p.w + (long long)bk * p.w_cols + t0 + tid;
+      *w += sum + reinterpret_cast<const float*>(smem + L::OFF_SUM)[tid];
+    }
+  }
+}
+
+template <int D>
+static cudaError_t launch_prefill_d(const AttnParams& p, const thrift_kv8_shape& s, cudaStream_t st) {
+  auto kern = prefill_kernel<D>;
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, PfLayout<D>::DYN);
+  if (e != cudaSuccess) return e;
+  kern<<<dim3(p.nsplit * p.row_tiles, s.B * s.Hkv), kPfThreads, PfLayout<D>::DYN, st>>>(p);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_prefill(const AttnParams& p, const thrift_kv8_shape& s, cudaStream_t st) {
+  return s.d == 128 ? launch_prefill_d<128>(p, s, st) : launch_prefill_d<64>(p, s, st);
+}
+
+template <int D>
+static cudaError_t launch_tile_weights_d(const AttnParams& p, const thrift_kv8_shape& s, cudaStream_t st) {
+  auto kern = tile_weights_kernel<D>;
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, TwLayout<D>::DYN);
+  if (e != cudaSuccess) return e;
+  kern<<<dim3((s.max_len + 127) / 128, s.B * s.Hkv), kTwThreads, TwLayout<D>::DYN, st>>>(p);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_tile_weights(const AttnParams& p, const thrift_kv8_shape& s, cudaStream_t st) {
+  return s.d == 128 ? launch_tile_weights_d<128>(p, s, st) : launch_tile_weights_d<64>(p, s, st);
+}
+
+}  // namespace kv8
+
+cudaError_t read_and_clear_kv8_prefill_error(uint32_t* word) { return kv8::read_and_clear_word(word); }
+
+}  // namespace thrift
