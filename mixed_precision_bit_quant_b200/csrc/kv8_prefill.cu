@@ -24,6 +24,7 @@ static_assert(2 * kPfSoftmaxRegs + kPfConvRegs + kPfOtherRegs <= 512, "register 
 constexpr uint64_t kPfWaitNs = 2000000000ull;  // 2 s per wait: far above any legitimate wait
 constexpr int kUp = 6;          // codes enter FP16 times 2^6: at most 448 * 64 < 65504
 constexpr float kPfLazy = 6.0f;  // a row's maximum is raised when exceeded by 2^6
+constexpr float kTiny = 1.17549435e-38f;  // a logit's scale is never 0: -inf times it stays -inf
 constexpr float kPfShift = 9.0f; // P enters FP16 times 2^9: at most 2^15
 
 enum PfBar : int { KFULL = 0, KEMPTY = 2, VFULL = 4, VEMPTY = 6, SFULL = 8, PFULL = 10, PVDONE = 12, DRAIN = 14, NPFBAR = 15 };
@@ -325,7 +326,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const AttnParams
       const int pos = r < r_cnt ? s.pos0 + (r_base + r) / p.G : -1;
       const int t_lo = s.pos0 + (r_base + tile * 128) / p.G;
       const int t_hi = s.pos0 + (r_base + min(r_cnt, tile * 128 + 128) - 1) / p.G;
-      const float sc = qscale * pow2f(max(-126, kref - 127 - kUp));
+      const float sc = fmaxf(qscale * pow2f(max(-126, kref - 127 - kUp)), kTiny);
       const bool bad_pages = misc[2] != 0;
       const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
       const uint32_t s_addr = lane_base + L::S_COL + 128 * tile, o_addr = lane_base + L::O_COL + D * tile;
@@ -646,7 +647,7 @@ __global__ void __launch_bounds__(kTwThreads, 1) tile_weights_kernel(const AttnP
       }
       // a row that sees nothing (lse = -inf) or is none gets -inf: its exponentials are 0
       float* rp = reinterpret_cast<float*>(smem + L::OFF_ROW + st * 1024) + 4 * (row >> 1) + (row & 1);
-      rp[0] = pow2f(e) * kf;
+      rp[0] = fmaxf(pow2f(e) * kf, kTiny);
       rp[2] = lse2 == -INFINITY ? -INFINITY : -lse2;
       fence_proxy_async_smem();
       __syncwarp();
