@@ -53,6 +53,19 @@ __device__ __forceinline__ Seq load_seq(const int32_t* lens, const int32_t* cu, 
   return s;
 }
 
+// 16-byte and 8-byte loads of read-only data that stay where they are written: an ordinary
+// load may be moved down to its first use, past the wait that it is meant to overlap.
+__device__ __forceinline__ uint4 ldg16_now(const void* a) {
+  uint4 u;
+  asm volatile("ld.global.nc.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w) : "l"(a));
+  return u;
+}
+__device__ __forceinline__ uint2 ldg8_now(const void* a) {
+  uint2 u;
+  asm volatile("ld.global.nc.v2.u32 {%0,%1}, [%2];" : "=r"(u.x), "=r"(u.y) : "l"(a));
+  return u;
+}
+
 // Two e4m3 codes (low byte first) -> f16x2, exact.
 __device__ __forceinline__ uint32_t e4m3x2_to_h2(uint32_t two) {
   uint32_t r;

@@ -90,7 +90,7 @@ __device__ __forceinline__ void load_k(const uint8_t* kp, int g, int t, uint4 (&
 #pragma unroll
   for (int r = 0; r < 2; ++r)
 #pragma unroll
-    for (int x = 0; x < D / 64; ++x) k[r][x] = __ldg(reinterpret_cast<const uint4*>(kp + (g + 8 * r) * D + 64 * x + 16 * t));
+    for (int x = 0; x < D / 64; ++x) k[r][x] = ldg16_now(kp + (g + 8 * r) * D + 64 * x + 16 * t);
 }
 template <int D>
 __device__ __forceinline__ void load_v(const uint8_t* vp, int g, int t, uint32_t (&v)[4][D / 32]) {
@@ -98,10 +98,10 @@ __device__ __forceinline__ void load_v(const uint8_t* vp, int g, int t, uint32_t
   for (int r = 0; r < 4; ++r) {
     const uint8_t* a = vp + (2 * t + (r & 1) + 8 * (r >> 1)) * D + g * (D / 8);
     if constexpr (D == 128) {
-      const uint4 u = __ldg(reinterpret_cast<const uint4*>(a));
+      const uint4 u = ldg16_now(a);
       v[r][0] = u.x; v[r][1] = u.y; v[r][2] = u.z; v[r][3] = u.w;
     } else {
-      const uint2 u = __ldg(reinterpret_cast<const uint2*>(a));
+      const uint2 u = ldg8_now(a);
       v[r][0] = u.x; v[r][1] = u.y;
     }
   }
@@ -211,13 +211,13 @@ __global__ void __launch_bounds__(kSplitThreads) split_kernel(const AttnParams p
     }
   };
   auto fetch = [&](int it, Codes<D>& c, int& pg) {
+    // loaded without a branch (page 0 for one that is not to be read): a load under a branch
+    // would be waited for where the branches join
     pg = __shfl_sync(0xffffffffu, l_page, it & 31);
-    if (pg >= 0) {
-      const int tok = span.token(v0 + warp + it * kSplitWarps);
-      const long long off = (((long long)pg * p.Hkv + hk) << p.page_log2) * D + (tok & page_mask) * D;
-      load_k<D>(p.k + off, g, t, c.k);
-      load_v<D>(p.v + off, g, t, c.v);
-    }
+    const int tok = span.token(v0 + warp + it * kSplitWarps);
+    const long long off = (((long long)max(pg, 0) * p.Hkv + hk) << p.page_log2) * D + (tok & page_mask) * D;
+    load_k<D>(p.k + off, g, t, c.k);
+    load_v<D>(p.v + off, g, t, c.v);
   };
   auto step = [&](int it, Codes<D>& c, int pg, int ksc, int vsc) {
     if (pg < 0) return;

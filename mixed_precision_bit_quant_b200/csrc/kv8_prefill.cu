@@ -182,41 +182,44 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const AttnParams
 
   if (warp >= 12) {
     regs_dec<kPfOtherRegs>();
-    if (warp == 12 && lane == 0) {
-      // ------------------------------------------------------------ issuer
-      bool ok = true;
+    if (warp == 12) {
+      // ------------------------------------------------------------ issuer (one converged warp)
+      const uint32_t el = elect_one(), tm = __shfl_sync(0xffffffffu, tmem, 0);
+      const uint32_t q_lo = desc_lo(sb + L::OFF_Q, 16), k_lo = desc_lo(sb + L::OFF_K, 16), v_lo = desc_lo(sb + L::OFF_V, 16384);
+      constexpr uint32_t HI = desc_hi(1024, SWZ_128B), TSTEP = L::TILE >> 4;
       auto qk = [&](int t, int st) {
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
-          const uint32_t off = (k >> 2) * 16384 + (k & 3) * 32;
-          mma_bf16_ss(tmem + L::S_COL + 128 * t, smem_desc(sb + L::OFF_Q + t * L::TILE + off, 16, 1024, SWZ_128B),
-                      smem_desc(sb + L::OFF_K + st * L::TILE + off, 16, 1024, SWZ_128B), idesc_f16(128, 0), k > 0);
+          const uint32_t off = ((k >> 2) * 16384 + (k & 3) * 32) >> 4;
+          mma_f16_ss_el(el, tm + L::S_COL + 128 * t, q_lo + t * TSTEP + off, HI, k_lo + st * TSTEP + off, HI,
+                        idesc_f16(128, 0), k > 0);
         }
-        tc_commit(BAR(SFULL + t));
+        tc_commit_el(el, BAR(SFULL + t));
       };
-      ok = mbar_wait(BAR(KFULL), 0, abort, kPfWaitNs);
+      auto wait = [&](int bar, int parity) -> bool {
+        return __all_sync(0xffffffffu, mbar_wait(BAR(bar), parity, abort, kPfWaitNs));
+      };
+      bool ok = wait(KFULL, 0);
       if (ok) {
         tc_fence_after();
         for (int t = 0; t < ntile; ++t) qk(t, 0);
-        tc_commit(BAR(KEMPTY));
+        tc_commit_el(el, BAR(KEMPTY));
       }
       for (int j = 0; ok && j < nj; ++j) {
         const int st = j & 1, sn = st ^ 1;
         for (int t = 0; t < ntile; ++t) {
-          if (!mbar_wait(BAR(PFULL + t), j & 1, abort, kPfWaitNs) ||
-              (t == 0 && !mbar_wait(BAR(VFULL + st), (j >> 1) & 1, abort, kPfWaitNs))) {
+          if (!wait(PFULL + t, j & 1) || (t == 0 && !wait(VFULL + st, (j >> 1) & 1))) {
             ok = false;
             break;
           }
           tc_fence_after();
 #pragma unroll
           for (int k = 0; k < 8; ++k)  // 16 tokens a step: 16 rows of 128 bytes
-            mma_bf16_ts(tmem + L::O_COL + D * t, tmem + L::S_COL + 128 * t + 8 * k,
-                        smem_desc(sb + L::OFF_V + st * L::TILE + 2048 * k, 16384, 1024, SWZ_128B), idesc_f16(D, 1),
-                        (j > 0 || k > 0) ? 1u : 0u);
-          tc_commit(BAR(PVDONE + t));
+            mma_f16_ts_el(el, tm + L::O_COL + D * t, tm + L::S_COL + 128 * t + 8 * k, v_lo + st * TSTEP + 128 * k, HI,
+                          idesc_f16(D, 1), (j > 0 || k > 0) ? 1u : 0u);
+          tc_commit_el(el, BAR(PVDONE + t));
           if (j + 1 < nj) {
-            if (t == 0 && !mbar_wait(BAR(KFULL + sn), ((j + 1) >> 1) & 1, abort, kPfWaitNs)) {
+            if (t == 0 && !wait(KFULL + sn, ((j + 1) >> 1) & 1)) {
               ok = false;
               break;
             }
@@ -224,11 +227,11 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const AttnParams
             qk(t, sn);
           }
         }
-        tc_commit(BAR(VEMPTY + st));
-        if (j + 1 < nj) tc_commit(BAR(KEMPTY + sn));
+        tc_commit_el(el, BAR(VEMPTY + st));
+        if (j + 1 < nj) tc_commit_el(el, BAR(KEMPTY + sn));
       }
-      if (!ok) pf_raise(abort);
-      tc_commit(BAR(DRAIN));  // every product issued above completes before TMEM is released
+      if (!ok && lane == 0) pf_raise(abort);
+      tc_commit_el(el, BAR(DRAIN));  // every product issued above completes before TMEM is released
       mbar_wait(BAR(DRAIN), 0, &never, kPfWaitNs);
     }
   } else if (warp >= 8) {
@@ -236,6 +239,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const AttnParams
     // -------------------------------------------------------------- converters
     constexpr int LPR = D / 16, RPI = 32 / LPR;  // lanes per token, tokens per load of a warp
     const int cw = warp - 8, c = lane % LPR, rr = lane / LPR;
+    const bool bad_pages = misc[2] != 0;
     // lane l of a batch: tile l / 2, group of 16 tokens 2 cw + (l & 1) of it
     int l_page = -1, l_ks = 0, l_vs = 0;
     auto batch = [&](int j0) {
@@ -253,25 +257,33 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const AttnParams
         }
       }
     };
+    // Unconditional loads (a group that is not to be read takes page 0 and is zeroed below): a
+    // load under a branch would be waited for where the branches join.
     auto load = [&](const uint8_t* base, int j, uint4 (&u)[LPR]) {
       const int tok = span.token(v0 + j) + 32 * cw;
 #pragma unroll
-      for (int i = 0; i < LPR; ++i) {
-        const int grp = i * RPI / 16;
-        const int pg = __shfl_sync(0xffffffffu, l_page, 2 * (j & 15) + grp);
-        u[i] = make_uint4(0, 0, 0, 0);
-        if (pg >= 0) {
-          const int slot = (tok + i * RPI + rr) & (page_tok - 1);
-          u[i] = __ldg(reinterpret_cast<const uint4*>(base + ((((long long)pg * p.Hkv + hk) << p.page_log2) + slot) * D) + c);
-        }
+      for (int g = 0; g < 2; ++g) {
+        const int pg = max(0, __shfl_sync(0xffffffffu, l_page, 2 * (j & 15) + g));
+        const uint8_t* at = base + ((((long long)pg * p.Hkv + hk) << p.page_log2) + ((tok + 16 * g) & (page_tok - 1)) + rr) * D + 16 * c;
+#pragma unroll
+        for (int i = 0; i < LPR / 2; ++i) u[g * (LPR / 2) + i] = ldg16_now(at + i * RPI * D);
       }
     };
-    // the loaded rows as FP16 into a tile; `edge`: rows that no query row sees become zero
-    auto store = [&](uint32_t dst, uint4 (&u)[LPR], const __half2 (&m)[2], bool edge, int tok) {
+    // the loaded rows as FP16 into a tile; where `edge` says so, rows that no query row sees or
+    // whose page is not of the pool become zero (their codes may be NaN)
+    auto store = [&](uint32_t dst, uint4 (&u)[LPR], const __half2 (&m)[2], bool edge, int tok, const bool (&held)[2]) {
+      if (edge) {
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+#pragma unroll
+          for (int i = 0; i < LPR / 2; ++i)
+            if (!held[g] || !any_visible(p, tok + 32 * cw + 16 * g + i * RPI + rr, 1, p_lo, p_hi))
+              u[g * (LPR / 2) + i] = make_uint4(0, 0, 0, 0);
+        }
+      }
 #pragma unroll
       for (int i = 0; i < LPR; ++i) {
         const int r = 32 * cw + i * RPI + rr;
-        if (edge && !any_visible(p, tok + r, 1, p_lo, p_hi)) u[i] = make_uint4(0, 0, 0, 0);
         const __half2 f = m[i * RPI / 16];
         const uint4 lo = make_uint4(hmul2_u32(e4m3x2_to_h2(u[i].x & 0xFFFFu), f), hmul2_u32(e4m3x2_to_h2(u[i].x >> 16), f),
                                     hmul2_u32(e4m3x2_to_h2(u[i].y & 0xFFFFu), f), hmul2_u32(e4m3x2_to_h2(u[i].y >> 16), f));
@@ -301,19 +313,20 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const AttnParams
     load(p.v, 0, uv);
     for (int j = 0; j < nj; ++j) {
       const int st = j & 1, use = j >> 1, tok = span.token(v0 + j);
-      const bool edge = !all_visible(p, tok, kPrefillTile, p_lo, p_hi);
+      const bool edge = bad_pages || !all_visible(p, tok, kPrefillTile, p_lo, p_hi);
       __half2 mk[2], mv[2];
+      const bool held[2] = {__shfl_sync(0xffffffffu, l_page, 2 * (j & 15)) >= 0, __shfl_sync(0xffffffffu, l_page, 2 * (j & 15) + 1) >= 0};
       factors(j, l_ks, kref, mk);
       factors(j, l_vs, vref, mv);
       if (use > 0 && !__all_sync(0xffffffffu, mbar_wait(BAR(KEMPTY + st), (use - 1) & 1, abort, kPfWaitNs))) { ok = false; break; }
-      store(sb + L::OFF_K + st * L::TILE, uk, mk, edge, tok);
+      store(sb + L::OFF_K + st * L::TILE, uk, mk, edge, tok, held);
       if (lane == 0) mbar_arrive(BAR(KFULL + st));
       if (j + 1 < nj) {
         if (((j + 1) & 15) == 0) batch(j + 1);
         load(p.k, j + 1, uk);
       }
       if (use > 0 && !__all_sync(0xffffffffu, mbar_wait(BAR(VEMPTY + st), (use - 1) & 1, abort, kPfWaitNs))) { ok = false; break; }
-      store(sb + L::OFF_V + st * L::TILE, uv, mv, edge, tok);
+      store(sb + L::OFF_V + st * L::TILE, uv, mv, edge, tok, held);
       if (lane == 0) mbar_arrive(BAR(VFULL + st));
       if (j + 1 < nj) load(p.v, j + 1, uv);
     }
