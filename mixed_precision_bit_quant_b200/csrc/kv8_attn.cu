@@ -6,9 +6,10 @@
 //
 // The query rows of one kv head's group are taken together: row r = i * G + g is
 // query head hk * G + g of new token i.  Kernels:
-//   split_kernel   one CTA per (tile of 8 or 16 rows, run of visible tokens, sequence and kv
-//                  head): online softmax over the run; writes the output, or the run's
-//                  state (maximum, sum, unnormalised output) when there are several runs
+//   split_kernel   few rows: every CTA takes the same share of all visible tokens of all tiles
+//                  of 8 or 16 rows; online softmax; writes the output, or a run's
+//                  state (maximum, sum, unnormalised output) where several CTAs share a tile
+//   prefill_kernel (kv8_prefill.cu) many rows
 //   merge_kernel   joins the runs' states of a row
 //   weights_kernel adds the rows' final weights to the running sums of the tokens
 #include "kv8_attn.cuh"
@@ -129,10 +130,79 @@ __device__ __forceinline__ void tile_logits(const uint4 (&k)[2][D / 64], const u
 constexpr float kLazy = 4.0f;  // a row's maximum is raised only when exceeded by 2^4
 constexpr int kPShift = 11;    // P enters FP16 times 2^11: at most 2^(4 + 11) = 2^15
 
-// One CTA per (row tile, run of visible tokens; sequence and kv head).  Each warp walks its
-// own tiles of 16 tokens straight from global memory into matrix fragments -- the codes'
-// layout in a page is the fragments' layout, so nothing is staged -- with the next tile's
-// loads in flight, and keeps its own softmax state; the warps' states are joined at the end.
+// The visible tokens of sequence b, in 16-token tiles, of one kv head: over the tiles of R rows.
+template <int R>
+__device__ __forceinline__ Span<kTile> row_tile_span(const AttnParams& p, const Seq& s, int rt) {
+  const int rows = min(s.nq * p.G - rt * R, R);
+  if (rows <= 0) return Span<kTile>{0, 0, 0};
+  return visible_span<kTile>(s.pos0 + rt * R / p.G, s.pos0 + (rt * R + rows - 1) / p.G, p.window, p.sinks);
+}
+
+// All tiles of the call in one line -- sequence, kv head, row tile, token -- of which every CTA
+// takes the same share (a multiple of kSplitWarps), so that sequences of any lengths load all
+// SMs evenly; the lengths are read here, not on the host.  A CTA's piece of one (sequence, kv
+// head, row tile), its unit, is a segment; segment cta + unit is its slot in the workspace
+// (both only grow along the line, so slots are distinct and below CTAs + units).
+struct Share {
+  long long at, end;  // this CTA's tiles
+  int b, share;       // the sequence of `at`; tiles of a CTA
+  long long b_at;     // the first tile of sequence b
+};
+template <int R>
+__device__ __forceinline__ Share find_share(const AttnParams& p, int B) {
+  __shared__ long long scan[kSplitWarps];
+  __shared__ Share found;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  long long total = 0;
+  // first pass: the number of tiles, hence the share; second pass: the sequence it starts in
+  for (int pass = 0; pass < 2; ++pass) {
+    long long base = 0;
+    for (int b0 = 0; b0 < B; b0 += kSplitThreads) {
+      const int b = b0 + threadIdx.x;
+      long long c = 0;
+      if (b < B) {
+        const Seq s = load_seq(p.lens, p.cu, b, p.n, p.max_q, p.max_len);
+        if (s.bad && pass == 0 && blockIdx.x == 0) raise_bad();
+        for (int rt = 0; rt < p.row_tiles; ++rt) c += row_tile_span<R>(p, s, rt).count;
+        c *= p.Hkv;
+      }
+      long long x = c;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+      }
+      __syncthreads();
+      if (lane == 31) scan[warp] = x;
+      __syncthreads();
+      long long before = base;
+#pragma unroll
+      for (int w = 0; w < kSplitWarps; ++w) {
+        if (w < warp) before += scan[w];
+        base += scan[w];
+      }
+      x += before;  // tiles up to and with sequence b
+      if (pass == 1 || B <= kSplitThreads) {
+        if (B <= kSplitThreads) total = base;
+        const long long each = (total + gridDim.x - 1) / gridDim.x;
+        const int share = (int)((each + kSplitWarps - 1) / kSplitWarps * kSplitWarps);
+        const long long at = (long long)blockIdx.x * share;
+        if (threadIdx.x == 0 && b0 == 0) found = Share{at, at, 0, share, 0};
+        __syncthreads();
+        if (at >= x - c && at < x) found = Share{at, min(total, at + share), b, share, x - c};
+      }
+    }
+    total = base;
+    if (B <= kSplitThreads) break;
+  }
+  __syncthreads();
+  return found;
+}
+
+// Each warp walks its own tiles of 16 tokens straight from global memory into matrix
+// fragments -- the codes' layout in a page is the fragments' layout, so nothing is staged --
+// with the next tile's loads in flight, and keeps its own softmax state; the warps' states are
+// joined at the end of a segment.
 //   S^T = K Q^T (m = tokens, n = rows): the e4m3 codes are exact in FP16; the page's scale,
 // the row's and the softmax's multiply the FP32 logits.
 //   O^T += V^T P^T: P goes to FP16 as p 2^(e_v - e_ref + 11), where e_v is the page's V exponent and
@@ -140,29 +210,14 @@ constexpr int kPShift = 11;    // P enters FP16 times 2^11: at most 2^(4 + 11) =
 // 8x8 transpose.  A row's maximum is raised (and O rescaled) only when a logit
 // exceeds it by 4 binades: the common step needs one vote and no cross-lane maximum.
 template <int D, int NT>
-__global__ void __launch_bounds__(kSplitThreads) split_kernel(const AttnParams p) {
+__device__ __forceinline__ void split_segment(const AttnParams& p, const Seq& s, int b, int hk, int rt, const Span<kTile>& span,
+                                              int v0, int v1, long long slot, float* sm) {
   constexpr int R = 8 * NT;
-  const int bk = blockIdx.y, b = bk / p.Hkv, hk = bk % p.Hkv;
-  const int split = blockIdx.x % p.nsplit, rt = blockIdx.x / p.nsplit;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const Seq s = load_seq(p.lens, p.cu, b, p.n, p.max_q, p.max_len);
-  if (s.bad && threadIdx.x == 0 && blockIdx.x == 0 && hk == 0) raise_bad();
-  const int rows = s.nq * p.G - rt * R;  // rows of this tile (may exceed R)
-  if (rows <= 0) return;
-  const int r_base = rt * R, r_cnt = min(rows, R);
+  const int r_base = rt * R, r_cnt = min(s.nq * p.G - r_base, R);
   const int p_lo = s.pos0 + r_base / p.G, p_hi = s.pos0 + (r_base + r_cnt - 1) / p.G;
-  const Span<kTile> span = visible_span<kTile>(p_lo, p_hi, p.window, p.sinks);
-  const int v0 = split * p.chunk, v1 = min(span.count, v0 + p.chunk);
-
-  extern __shared__ __align__(16) float sm[];
   float* so = sm;                              // [warps][R][D + 4]
   float* sml = sm + kSplitWarps * R * (D + 4);  // [warps][R][2]
-
-  if (v0 >= v1 && (p.nsplit > 1)) {  // nothing in this run: an empty state
-    for (int r = threadIdx.x; r < r_cnt; r += kSplitThreads)
-      p.part_ml[packed_row(p, s, hk, r_base + r) * p.nsplit + split] = make_float2(-INFINITY, 0.0f);
-    return;
-  }
 
   uint32_t qf[NT][D / 16][2];
   float fs[NT][2];   // per column 2t, 2t+1: logits' scale without the page's
@@ -371,51 +426,144 @@ __global__ void __launch_bounds__(kSplitThreads) split_kernel(const AttnParams p
       o.z += x.z * f;
       o.w += x.w * f;
     }
-    const long long row = packed_row(p, s, hk, r_base + r);
-    if (p.nsplit == 1) {
+    if (slot < 0) {  // the whole unit: final
+      const long long row = packed_row(p, s, hk, r_base + r);
       const float inv = ll > 0.0f ? 1.0f / ll : 0.0f;
       reinterpret_cast<uint2*>(p.o)[row * (D / 4) + c4] =
           make_uint2(float2_to_pair(o.x * inv, o.y * inv, p.fp16), float2_to_pair(o.z * inv, o.w * inv, p.fp16));
       if (c4 == 0) write_lse(p, row, mm, ll);
     } else {
-      *reinterpret_cast<float4*>(p.part_o + (row * p.nsplit + split) * D + 4 * c4) = o;
-      if (c4 == 0) p.part_ml[row * p.nsplit + split] = make_float2(mm, ll);
+      *reinterpret_cast<float4*>(p.part_o + (slot * R + r) * D + 4 * c4) = o;
+      if (c4 == 0) p.part_ml[slot * R + r] = make_float2(mm, ll);
     }
   }
 }
 
-// One CTA per new token of a sequence, a warp per query head: the runs' states joined, a
-// lane's D / 32 channels in registers.
-template <int D>
-__global__ void __launch_bounds__(128) merge_kernel(const AttnParams p) {
-  constexpr int C = D / 32;
-  const int lane = threadIdx.x & 31;
-  const Seq s = load_seq(p.lens, p.cu, blockIdx.y, p.n, p.max_q, p.max_len);
-  if ((int)blockIdx.x >= s.nq) return;
-  for (int h = threadIdx.x >> 5; h < p.Hq; h += 4) {
-    const long long row = (long long)(s.q0 + blockIdx.x) * p.Hq + h;
-    const float2* ml = p.part_ml + row * p.nsplit;
-    float mm = -INFINITY;
-    for (int i = lane; i < p.nsplit; i += 32) mm = fmaxf(mm, ml[i].x);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, o));
-    float ll = 0.0f, acc[C];
-#pragma unroll
-    for (int c = 0; c < C; ++c) acc[c] = 0.0f;
-    for (int i = 0; i < p.nsplit; ++i) {
-      const float2 x = ml[i];
-      if (x.x == -INFINITY) continue;  // an empty run wrote no output
-      const float f = ex2_approx(x.x - mm);
-      ll += x.y * f;
-      const float* y = p.part_o + (row * p.nsplit + i) * D + lane * C;
-#pragma unroll
-      for (int c = 0; c < C; ++c) acc[c] += y[c] * f;
+// CTAs that an SM holds (their registers), of which the plan launches one wave.
+__host__ __device__ constexpr int resident_ctas(int d, int nt) { return d == 128 ? (nt == 1 ? 3 : 2) : (nt == 1 ? 4 : 3); }
+
+template <int D, int NT>
+__global__ void __launch_bounds__(kSplitThreads, resident_ctas(D, NT)) split_kernel(const AttnParams p, int B) {
+  constexpr int R = 8 * NT;
+  extern __shared__ __align__(16) float sm[];
+  const Share sh = find_share<R>(p, B);
+  long long at = sh.at, b_at = sh.b_at;
+  for (int b = sh.b; at < sh.end && b < B; ++b) {
+    const Seq s = load_seq(p.lens, p.cu, b, p.n, p.max_q, p.max_len);
+    int per_head = 0;  // tiles of one kv head
+    for (int rt = 0; rt < p.row_tiles; ++rt) per_head += row_tile_span<R>(p, s, rt).count;
+    const long long b_end = b_at + (long long)per_head * p.Hkv;
+    while (at < sh.end && at < b_end) {
+      const int hk = (int)((at - b_at) / per_head);
+      int v = (int)((at - b_at) % per_head), rt = 0;
+      Span<kTile> span = row_tile_span<R>(p, s, 0);
+      while (v >= span.count) {
+        v -= span.count;
+        span = row_tile_span<R>(p, s, ++rt);
+      }
+      const int v1 = (int)min((long long)span.count, v + (sh.end - at));
+      const int unit = (b * p.Hkv + hk) * p.row_tiles + rt;
+      const bool whole = v == 0 && v1 == span.count;
+      if (v == 0 && threadIdx.x == 0) {  // the unit's first slot and how many it has
+        const long long u_at = at, last = u_at + span.count - 1;
+        p.unit_slots[unit] = make_int2((int)blockIdx.x + unit, (int)(last / sh.share - u_at / sh.share) + 1);
+      }
+      split_segment<D, NT>(p, s, b, hk, rt, span, v, v1, whole ? -1 : (long long)blockIdx.x + unit, sm);
+      at += v1 - v;
+      __syncthreads();  // shared memory is free again
     }
-    const float inv = ll > 0.0f ? 1.0f / ll : 0.0f;
-    uint32_t* o = static_cast<uint32_t*>(p.o) + row * (D / 2) + lane * (C / 2);
+    b_at = b_end;
+  }
+}
+
+// Joins the runs' states of a row: one CTA per (new token and query head, sequence).  The
+// warps share the runs, four loads in flight each (a warp alone took 40 us for 64 runs: one
+// dependent load after the other), and are joined in shared memory.  Run order and warp
+// order are fixed, so the sum is.  R: rows of split_kernel's tiles, or 0 where prefill_kernel
+// cut the call into p.nsplit runs per row.
+constexpr int kMergeWarps = 4;
+template <int D, int R>
+__global__ void __launch_bounds__(32 * kMergeWarps) merge_kernel(const AttnParams p) {
+  constexpr int C = D / 32;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const Seq s = load_seq(p.lens, p.cu, blockIdx.y, p.n, p.max_q, p.max_len);
+  const int i = blockIdx.x / p.Hq, h = blockIdx.x % p.Hq;
+  if (i >= s.nq) return;
+  const long long row = (long long)(s.q0 + i) * p.Hq + h;
+  // state k of the row is element first + k * step
+  long long first, step;
+  int count;
+  if constexpr (R == 0) {
+    first = row * p.nsplit;
+    step = 1;
+    count = p.nsplit;
+  } else {
+    const int r = i * p.G + h % p.G, rt = r / R;
+    if (row_tile_span<R>(p, s, rt).count == 0) {  // no row of the tile sees anything: no segment
+      if (threadIdx.x < D / 2) static_cast<uint32_t*>(p.o)[row * (D / 2) + threadIdx.x] = 0u;
+      if (threadIdx.x == 0) write_lse(p, row, -INFINITY, 0.0f);
+      return;
+    }
+    const int2 slots = p.unit_slots[(blockIdx.y * p.Hkv + h / p.G) * p.row_tiles + rt];
+    if (slots.y == 1) return;  // written by its only segment
+    first = (long long)slots.x * R + r % R;
+    step = R;
+    count = slots.y;
+  }
+  const float2* ml = p.part_ml + first;
+  const float* po = p.part_o + first * D + lane * C;
+  __shared__ float so[kMergeWarps][D];
+  __shared__ float sl[kMergeWarps];
+  float mm = -INFINITY;
+  for (int k = lane; k < count; k += 32) mm = fmaxf(mm, ml[k * step].x);
 #pragma unroll
-    for (int c = 0; c < C; c += 2) o[c / 2] = float2_to_pair(acc[c] * inv, acc[c + 1] * inv, p.fp16);
-    if (lane == 0) write_lse(p, row, mm, ll);
+  for (int o = 16; o > 0; o >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, o));
+  float ll = 0.0f, acc[C];
+#pragma unroll
+  for (int c = 0; c < C; ++c) acc[c] = 0.0f;
+  for (int k0 = warp; k0 < count; k0 += 4 * kMergeWarps) {
+    float x[4][C], f[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int k = k0 + u * kMergeWarps;
+      f[u] = 0.0f;
+#pragma unroll
+      for (int c = 0; c < C; ++c) x[u][c] = 0.0f;
+      if (k < count) {
+        const float2 y = ml[k * step];
+        if (y.x != -INFINITY) {  // an empty run wrote no output
+          f[u] = ex2_approx(y.x - mm);
+          ll += y.y * f[u];
+          if constexpr (C == 4) {
+            const float4 z = *reinterpret_cast<const float4*>(po + k * step * D);
+            x[u][0] = z.x; x[u][1] = z.y; x[u][2] = z.z; x[u][3] = z.w;
+          } else {
+            const float2 z = *reinterpret_cast<const float2*>(po + k * step * D);
+            x[u][0] = z.x; x[u][1] = z.y;
+          }
+        }
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+#pragma unroll
+      for (int c = 0; c < C; ++c) acc[c] += x[u][c] * f[u];
+  }
+#pragma unroll
+  for (int c = 0; c < C; ++c) so[warp][lane * C + c] = acc[c];
+  if (lane == 0) sl[warp] = ll;
+  __syncthreads();
+  if (threadIdx.x < D / 2) {
+    float l = 0.0f, a = 0.0f, b = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kMergeWarps; ++w) {
+      l += sl[w];
+      a += so[w][2 * threadIdx.x];
+      b += so[w][2 * threadIdx.x + 1];
+    }
+    const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+    static_cast<uint32_t*>(p.o)[row * (D / 2) + threadIdx.x] = float2_to_pair(a * inv, b * inv, p.fp16);
+    if (threadIdx.x == 0) write_lse(p, row, mm, l);
   }
 }
 
@@ -492,41 +640,48 @@ static Plan make_plan(const thrift_kv8_shape& s, const thrift_kv8_mask& m, bool 
     p.chunk = (int)((tiles + ns - 1) / ns);
     if (p.chunk < 2) p.chunk = 2;
   } else {
-    long long ns = (148 * 4) / units;
-    const long long most = (tiles + kSplitWarps - 1) / kSplitWarps;
-    ns = ns < 1 ? 1 : (ns > most ? most : ns);
-    if (ns > 64) ns = 64;
-    p.chunk = (int)(((tiles + ns - 1) / ns + kSplitWarps - 1) / kSplitWarps * kSplitWarps);
+    const int resident = resident_ctas(s.d, p.nt);
+    const long long most = (tiles * units + kSplitWarps - 1) / kSplitWarps;
+    p.ctas = (int)(most < 148 * resident ? most : 148 * resident);
   }
-  p.nsplit = (int)((tiles + p.chunk - 1) / p.chunk);
   const size_t nrow = (size_t)s.n * s.Hq;
-  p.ml_off = 0;
-  p.o_off = p.nsplit > 1 ? (nrow * p.nsplit * sizeof(float2) + 255) / 256 * 256 : 0;
-  p.lse_off = p.nsplit > 1 ? p.o_off + nrow * p.nsplit * s.d * sizeof(float) : 0;
-  p.bytes = p.lse_off + (with_w ? nrow * sizeof(float) : 0);
+  size_t states, at = 0;
+  if (p.tiles128) {
+    p.nsplit = (int)((tiles + p.chunk - 1) / p.chunk);
+    states = p.nsplit > 1 ? nrow * p.nsplit : 0;
+  } else {
+    p.nsplit = 0;
+    states = (size_t)(p.ctas + units) * R;
+  }
+  auto take = [&](size_t n) { const size_t o = at; at += (n + 255) / 256 * 256; return o; };
+  p.ml_off = take(states * sizeof(float2));
+  p.o_off = take(states * s.d * sizeof(float));
+  p.slots_off = take(p.tiles128 ? 0 : (size_t)units * sizeof(int2));
+  p.lse_off = take(with_w ? nrow * sizeof(float) : 0);
+  p.bytes = at;
   return p;
 }
 
 template <int D, int NT>
-static void launch_split(const AttnParams& p, dim3 grid, cudaStream_t s) {
+static void launch_split(const AttnParams& p, const Plan& plan, const thrift_kv8_shape& s, cudaStream_t st) {
   constexpr int sm = (int)sizeof(float) * kSplitWarps * 8 * NT * (D + 4 + 2);
-  split_kernel<D, NT><<<grid, kSplitThreads, sm, s>>>(p);
+  split_kernel<D, NT><<<plan.ctas, kSplitThreads, sm, st>>>(p, s.B);
+  merge_kernel<D, 8 * NT><<<dim3(s.max_q * s.Hq, s.B), 32 * kMergeWarps, 0, st>>>(p);
 }
 
 template <int D>
 static cudaError_t launch_attn_d(const AttnParams& p, const Plan& plan, const thrift_kv8_shape& s, cudaStream_t st) {
-  const dim3 grid(plan.nsplit * plan.row_tiles, s.B * s.Hkv);
   int launches = 1;
   if (plan.tiles128) {
     const cudaError_t e = launch_prefill(p, s, st);
     if (e != cudaSuccess) return e;
-  } else if (plan.nt == 1) {
-    launch_split<D, 1>(p, grid, st);
+    if (plan.nsplit > 1) {
+      merge_kernel<D, 0><<<dim3(s.max_q * s.Hq, s.B), 32 * kMergeWarps, 0, st>>>(p);
+      ++launches;
+    }
   } else {
-    launch_split<D, 2>(p, grid, st);
-  }
-  if (plan.nsplit > 1) {
-    merge_kernel<D><<<dim3(s.max_q, s.B), 128, 0, st>>>(p);
+    if (plan.nt == 1) launch_split<D, 1>(p, plan, s, st);
+    else launch_split<D, 2>(p, plan, s, st);
     ++launches;
   }
   if (p.w != nullptr && plan.tiles128) {
@@ -559,6 +714,7 @@ cudaError_t launch_kv8_attn(const Kv8Args& a, const Kv8Attn& t, cudaStream_t st)
   uint8_t* ws = static_cast<uint8_t*>(t.ws);
   p.part_ml = reinterpret_cast<float2*>(ws + plan.ml_off);
   p.part_o = reinterpret_cast<float*>(ws + plan.o_off);
+  p.unit_slots = reinterpret_cast<int2*>(ws + plan.slots_off);
   p.w = t.w; p.w_cols = t.w_cols;
   p.lse2 = t.w != nullptr ? reinterpret_cast<float*>(ws + plan.lse_off) : nullptr;
   p.Hq = a.s.Hq; p.Hkv = a.s.Hkv; p.G = a.s.Hq / a.s.Hkv;

@@ -14,13 +14,16 @@ struct AttnParams {
   const int32_t *table, *lens, *cu;
   void* o;
   float* lse;
-  float2* part_ml;  // [row][nsplit] maximum (log2 domain) and sum
-  float* part_o;    // [row][nsplit][D]
+  // states of runs: maximum (log2 domain) and sum, and the unnormalised output; element
+  // row * nsplit + run (prefill_kernel) or slot * R + row of the tile (split_kernel)
+  float2* part_ml;
+  float* part_o;
+  int2* unit_slots;  // split_kernel: first slot and slots of a (sequence, kv head, row tile)
   float* lse2;      // [row] log2-domain log-sum-exp for the weights (or null)
   float* w;
   long long w_cols;
   int Hq, Hkv, G, page_log2, table_cols, n, max_q, max_len, num_pages, window, sinks, fp16;
-  int nsplit, chunk, row_tiles;  // chunk: 16-token tiles of a run
+  int nsplit, chunk, row_tiles;  // prefill_kernel: runs per row, 128-token tiles of a run
   float scale_log2;
 };
 
@@ -74,8 +77,8 @@ __device__ __forceinline__ bool all_visible(const AttnParams& p, int a, int n, i
 // How a call is cut up.  The same for the workspace's size and the launch.
 struct Plan {
   bool tiles128;  // prefill_kernel (128-row tiles) instead of split_kernel
-  int nt, row_tiles, nsplit, chunk;
-  size_t ml_off, o_off, lse_off, bytes;
+  int nt, row_tiles, nsplit, chunk, ctas;
+  size_t ml_off, o_off, slots_off, lse_off, bytes;
 };
 
 cudaError_t launch_prefill(const AttnParams& p, const thrift_kv8_shape& s, cudaStream_t st);
