@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import dataclasses
+import functools
 import os
 from typing import Optional
 
@@ -433,7 +434,7 @@ class Kv8Cache:
     """A pool of 8-bit pages: k, v uint8 [num_pages, Hkv, page, d] (e4m3 codes), ks, vs uint8
     [num_pages, Hkv] (the exponent of a page and kv head, plus 127)."""
 
-    __slots__ = ("k", "v", "ks", "vs", "num_pages", "Hkv", "page", "d", "device", "_struct")
+    __slots__ = ("k", "v", "ks", "vs", "num_pages", "Hkv", "page", "d", "device", "_ref")
 
     def __init__(self, k: torch.Tensor, v: torch.Tensor, ks: torch.Tensor, vs: torch.Tensor):
         if not isinstance(k, torch.Tensor) or k.dim() != 4:
@@ -447,7 +448,8 @@ class Kv8Cache:
         if int(lib().thrift_kv8_cache_bytes(self.num_pages, self.Hkv, self.page, self.d, 0)) == 0:
             raise ThriftError(THRIFT_ERR_UNSUPPORTED, "thrift_kv8_cache_bytes")
         self.device = k.device
-        self._struct = Kv8CacheStruct(k.data_ptr(), v.data_ptr(), ks.data_ptr(), vs.data_ptr(), self.num_pages)
+        self._ref = ctypes.byref(Kv8CacheStruct(k.data_ptr(), v.data_ptr(), ks.data_ptr(), vs.data_ptr(),
+                                                self.num_pages))
 
 
 def kv8_alloc(num_pages: int, Hkv: int, page: int, d: int, device) -> Kv8Cache:
@@ -471,11 +473,14 @@ def _kv8_tokens(x: torch.Tensor, name: str, heads: int, d: int, device) -> int:
     n, h, w = x.shape
     if w != d or (heads and h != heads):
         raise ValueError(f"{name}: shape {tuple(x.shape)}, expected (n, {heads or 'Hq'}, {d})")
+    if x.device != device or device.type != "cuda":
+        _on_device(x, name, device)
+    if x.is_contiguous():
+        return h * d
     st, sh, sd = x.stride()
-    if n > 0 and (sd != 1 or (sh != d and h != 1) or (st % 8 and n != 1)):
+    if sd != 1 or (sh != d and h != 1) or (st % 8 and n != 1):
         raise ValueError(f"{name}: heads and channels must be contiguous and the token stride a multiple of 8")
-    _on_device(x, name, device)
-    return h * d if n <= 1 else st
+    return h * d if n == 1 else st
 
 
 def _kv8_ints(t: torch.Tensor, name: str, shape, device) -> int:
@@ -484,12 +489,26 @@ def _kv8_ints(t: torch.Tensor, name: str, shape, device) -> int:
     if t.dtype is not torch.int32 or t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name}: expected a contiguous torch.int32 tensor of shape {tuple(shape)}, "
                          f"got {t.dtype} {tuple(t.shape)}")
-    _on_device(t, name, device)
+    if t.device != device or device.type != "cuda":
+        _on_device(t, name, device)
     return t.data_ptr()
 
 
-def _kv8_shape(cache: Kv8Cache, table, lens, cu, n, Hq, max_q, max_len, dtype):
-    """The shape struct and the pointers of table, lens and cu."""
+@functools.lru_cache(maxsize=4096)
+def _kv8_args(B, Hq, Hkv, d, page, cols, n, max_q, max_len, dtype, window=0, sinks=0, softmax_scale=0.0, with_w=None):
+    """The structs of a call with these numbers, as they are passed, and (for attention) the bytes of workspace.
+    They depend on nothing else, so a serving loop makes them once."""
+    numbers = (B, Hq, Hkv, d, page, cols, n, max_q, max_len, dtype)
+    for x in numbers + (window, sinks):
+        if not -2 ** 31 <= x < 2 ** 31:
+            raise ValueError(f"{x}: does not fit 32 bits")
+    shape, mask = ctypes.byref(Kv8Shape(*numbers)), ctypes.byref(Kv8Mask(window, sinks, softmax_scale))
+    need = 0 if with_w is None else int(lib().thrift_kv8_attn_workspace_bytes(shape, mask, with_w))
+    return shape, mask, need
+
+
+def _kv8_rows(cache: Kv8Cache, table, lens, cu, n, max_q, max_len):
+    """B, the columns of table, the bounds, and the pointers of table, lens and cu."""
     if not isinstance(table, torch.Tensor) or table.dim() != 2:
         raise ValueError("table: expected a [B, pages] tensor")
     B, cols = table.shape
@@ -500,8 +519,7 @@ def _kv8_shape(cache: Kv8Cache, table, lens, cu, n, Hq, max_q, max_len, dtype):
     if cu is None and n != B:
         raise ValueError(f"{n} rows for {B} sequences: without cu each sequence has one new token")
     max_q = (1 if cu is None else n) if max_q is None else int(max_q)
-    max_len = cols * cache.page if max_len is None else int(max_len)
-    return Kv8Shape(B, Hq, cache.Hkv, cache.d, cache.page, cols, n, max_q, max_len, dtype), tp, lp, cp
+    return B, cols, max_q, cols * cache.page if max_len is None else int(max_len), tp, lp, cp
 
 
 def _kv8_call(fn, what: str, device, *args) -> None:
@@ -526,9 +544,11 @@ def kv8_append(cache: Kv8Cache, k: torch.Tensor, v: torch.Tensor, table: torch.T
     vs = _kv8_tokens(v, "v", cache.Hkv, cache.d, cache.device)
     if v.dtype is not k.dtype or v.shape != k.shape:
         raise ValueError("v: expected the dtype and shape of k")
-    shape, tp, lp, cp = _kv8_shape(cache, table, lens, cu, k.shape[0], cache.Hkv, max_q, None, _KV8_DTYPES[k.dtype])
-    _kv8_call(lib().thrift_kv8_append, "thrift_kv8_append", cache.device, ctypes.byref(shape),
-              ctypes.byref(cache._struct), k.data_ptr(), ks, v.data_ptr(), vs, tp, lp, cp)
+    n = k.shape[0]
+    B, cols, max_q, max_len, tp, lp, cp = _kv8_rows(cache, table, lens, cu, n, max_q, None)
+    shape, _, _ = _kv8_args(B, cache.Hkv, cache.Hkv, cache.d, cache.page, cols, n, max_q, max_len, _KV8_DTYPES[k.dtype])
+    _kv8_call(lib().thrift_kv8_append, "thrift_kv8_append", cache.device, shape, cache._ref, k.data_ptr(), ks,
+              v.data_ptr(), vs, tp, lp, cp)
 
 
 def _kv8_weights(w: torch.Tensor, name: str, B: int, Hkv: int, device) -> int:
@@ -536,7 +556,8 @@ def _kv8_weights(w: torch.Tensor, name: str, B: int, Hkv: int, device) -> int:
         raise ValueError(f"{name}: expected a [B, Hkv, columns] tensor for B = {B}, Hkv = {Hkv}")
     if w.dtype is not torch.float32 or not w.is_contiguous():
         raise ValueError(f"{name}: expected a contiguous torch.float32 tensor")
-    _on_device(w, name, device)
+    if w.device != device or device.type != "cuda":
+        _on_device(w, name, device)
     return w.shape[2]
 
 
@@ -553,30 +574,30 @@ def kv8_attention(q: torch.Tensor, cache: Kv8Cache, table: torch.Tensor, lens: t
     _want_kv8(cache, "cache")
     qs = _kv8_tokens(q, "q", 0, cache.d, cache.device)
     n, Hq, d = q.shape
-    shape, tp, lp, cp = _kv8_shape(cache, table, lens, cu, n, Hq, max_q, max_len, _KV8_DTYPES[q.dtype])
+    B, cols, max_q, max_len, tp, lp, cp = _kv8_rows(cache, table, lens, cu, n, max_q, max_len)
     dev = cache.device
-    mask = Kv8Mask(window, sinks, softmax_scale)
-    w_cols = 0
+    w_cols, wp = 0, None
     if weights is not None:
-        w_cols = _kv8_weights(weights, "weights", shape.B, cache.Hkv, dev)
+        w_cols, wp = _kv8_weights(weights, "weights", B, cache.Hkv, dev), weights.data_ptr()
+    shape, mask, need = _kv8_args(B, Hq, cache.Hkv, d, cache.page, cols, n, max_q, max_len, _KV8_DTYPES[q.dtype],
+                                  window, sinks, softmax_scale, wp is not None)
     if o is None:
-        o = torch.empty((n, Hq, d), dtype=q.dtype, device=dev)
+        o = torch.empty_like(q, memory_format=torch.contiguous_format)
     else:
         _want(o, "o", q.dtype, (n, Hq, d), dev)
     if lse is not None:
         _want(lse, "lse", torch.float32, (n, Hq), dev)
     elif want_lse:
-        lse = torch.empty((n, Hq), dtype=torch.float32, device=dev)
-    need = int(lib().thrift_kv8_attn_workspace_bytes(ctypes.byref(shape), ctypes.byref(mask), weights is not None))
+        lse = q.new_empty((n, Hq), dtype=torch.float32)
     if ws is not None:
         _want(ws, "ws", torch.uint8, device=dev)
         if ws.numel() < need:
             raise ValueError(f"ws: {ws.numel()} bytes, the call needs {need}")
     elif need:
         ws = torch.empty(need, dtype=torch.uint8, device=dev)
-    _kv8_call(lib().thrift_kv8_attn, "thrift_kv8_attn", dev, ctypes.byref(shape), ctypes.byref(mask),
-              ctypes.byref(cache._struct), q.data_ptr(), qs, tp, lp, cp, o.data_ptr(), _ptr(lse), _ptr(weights),
-              w_cols, _ptr(ws), 0 if ws is None else ws.numel())
+    _kv8_call(lib().thrift_kv8_attn, "thrift_kv8_attn", dev, shape, mask, cache._ref, q.data_ptr(), qs, tp, lp, cp,
+              o.data_ptr(), None if lse is None else lse.data_ptr(), wp, w_cols, None if ws is None else ws.data_ptr(),
+              need)
     return o, lse
 
 
@@ -587,9 +608,9 @@ def kv8_attention_workspace(q: torch.Tensor, cache: Kv8Cache, table: torch.Tenso
     """thrift_kv8_attn_workspace_bytes of a kv8_attention call with these arguments."""
     _want_kv8(cache, "cache")
     _kv8_tokens(q, "q", 0, cache.d, cache.device)
-    shape = _kv8_shape(cache, table, lens, cu, q.shape[0], q.shape[1], max_q, max_len, _KV8_DTYPES[q.dtype])[0]
-    mask = Kv8Mask(window, sinks, 0.0)
-    return int(lib().thrift_kv8_attn_workspace_bytes(ctypes.byref(shape), ctypes.byref(mask), weights is not None))
+    B, cols, max_q, max_len, _, _, _ = _kv8_rows(cache, table, lens, cu, q.shape[0], max_q, max_len)
+    return _kv8_args(B, q.shape[1], cache.Hkv, cache.d, cache.page, cols, q.shape[0], max_q, max_len,
+                     _KV8_DTYPES[q.dtype], window, sinks, 0.0, weights is not None)[2]
 
 
 def kv8_evict(cache: Kv8Cache, table: torch.Tensor, lens: torch.Tensor, weights: torch.Tensor, dst: Kv8Cache,
@@ -602,8 +623,10 @@ def kv8_evict(cache: Kv8Cache, table: torch.Tensor, lens: torch.Tensor, weights:
     none that the call reads; dst_weights must not overlap weights."""
     _want_kv8(cache, "cache")
     _want_kv8(dst, "dst")
-    shape, tp, lp, _ = _kv8_shape(cache, table, lens, None, table.shape[0], cache.Hkv, 1, max_len, 0)
-    dev, B, Hkv = cache.device, shape.B, cache.Hkv
+    dev, Hkv = cache.device, cache.Hkv
+    n = table.shape[0] if isinstance(table, torch.Tensor) else 0
+    B, cols, max_q, max_len, tp, lp, _ = _kv8_rows(cache, table, lens, None, n, 1, max_len)
+    shape, _, _ = _kv8_args(B, Hkv, Hkv, cache.d, cache.page, cols, B, max_q, max_len, 0)
     if (dst.Hkv, dst.page, dst.d, dst.device) != (Hkv, cache.page, cache.d, dev):
         raise ValueError("dst: expected a Kv8Cache with the heads, page, d and device of cache")
     if not isinstance(dst_table, torch.Tensor) or dst_table.dim() != 2:
@@ -614,13 +637,15 @@ def kv8_evict(cache: Kv8Cache, table: torch.Tensor, lens: torch.Tensor, weights:
     a, b = weights.data_ptr(), dst_weights.data_ptr()
     if a < b + 4 * dst_weights.numel() and b < a + 4 * weights.numel():
         raise ValueError("dst_weights: must not overlap weights")
-    keep = int(keep)
+    keep, sinks, recent = int(keep), int(sinks), int(recent)
+    if not all(-2 ** 31 <= x < 2 ** 31 for x in (keep, sinks, recent)):
+        raise ValueError("keep, sinks, recent: must fit 32 bits")
     if dst_lens is None:
         dst_lens = torch.empty((B,), dtype=torch.int32, device=dev)
     if kept is None:
         kept = torch.empty((B, Hkv, max(keep, 0)), dtype=torch.int32, device=dev)
-    _kv8_call(lib().thrift_kv8_evict, "thrift_kv8_evict", dev, ctypes.byref(shape), ctypes.byref(cache._struct), tp,
-              lp, a, w_cols, keep, int(sinks), int(recent), ctypes.byref(dst._struct), dtp, dst_table.shape[1],
+    _kv8_call(lib().thrift_kv8_evict, "thrift_kv8_evict", dev, shape, cache._ref, tp, lp, a, w_cols, keep, sinks,
+              recent, dst._ref, dtp, dst_table.shape[1],
               _kv8_ints(dst_lens, "dst_lens", (B,), dev), b, dw_cols, _kv8_ints(kept, "kept", (B, Hkv, keep), dev))
     return dst_lens, kept
 

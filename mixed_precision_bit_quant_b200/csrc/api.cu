@@ -316,6 +316,10 @@ static int check_kv8_shape(const thrift_kv8_shape* s, bool with_q) {
   if (s->max_len > cap || s->max_q > s->n) return THRIFT_ERR_INVALID;
   if (cap > (1 << 24) || (long long)s->B * s->Hkv > 65535) return THRIFT_ERR_UNSUPPORTED;
   if (with_q && (long long)s->n * s->Hq > 0x7FFFFFFFLL) return THRIFT_ERR_UNSUPPORTED;
+  // 16-token tiles of all sequences, kv heads and tiles of 8 rows are counted in 32 bits
+  if (with_q && (long long)s->B * s->Hkv * (((long long)s->max_q * (s->Hq / s->Hkv) + 7) / 8) * ((s->max_len + 15) / 16 + 1) > 0x7FFFFFFFLL &&
+      (long long)s->max_q * (s->Hq / s->Hkv) <= 64)
+    return THRIFT_ERR_UNSUPPORTED;
   // the kernels' grids: rows of a sequence (new tokens times query heads of a group), kv heads twice
   if (with_q && (long long)s->max_q * (s->Hq / s->Hkv) > (1 << 24)) return THRIFT_ERR_UNSUPPORTED;
   if (2LL * s->Hkv > 65535) return THRIFT_ERR_UNSUPPORTED;

@@ -144,56 +144,57 @@ __device__ __forceinline__ Span<kTile> row_tile_span(const AttnParams& p, const 
 // head, row tile), its unit, is a segment; segment cta + unit is its slot in the workspace
 // (both only grow along the line, so slots are distinct and below CTAs + units).
 struct Share {
-  long long at, end;  // this CTA's tiles
-  int b, share;       // the sequence of `at`; tiles of a CTA
-  long long b_at;     // the first tile of sequence b
+  int at, end;      // this CTA's tiles (the host bounds their number below 2^31)
+  int share;        // tiles of a CTA
+  int b, b_at, b_c; // the sequence of `at`, its first tile and its tiles
+  Seq s;
 };
 template <int R>
 __device__ __forceinline__ Share find_share(const AttnParams& p, int B) {
-  __shared__ long long scan[kSplitWarps];
+  __shared__ int scan[kSplitWarps];
   __shared__ Share found;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  long long total = 0;
+  if (threadIdx.x == 0) found.at = found.end = 0;
   // first pass: the number of tiles, hence the share; second pass: the sequence it starts in
-  for (int pass = 0; pass < 2; ++pass) {
-    long long base = 0;
+  // (one pass finds both where the CTA's threads hold all sequences)
+  int total = 0;
+  for (int pass = B <= kSplitThreads ? 1 : 0; pass < 2; ++pass) {
+    int base = 0;
     for (int b0 = 0; b0 < B; b0 += kSplitThreads) {
       const int b = b0 + threadIdx.x;
-      long long c = 0;
+      int c = 0;
+      Seq s{0, 0, 0, 0, false};
       if (b < B) {
-        const Seq s = load_seq(p.lens, p.cu, b, p.n, p.max_q, p.max_len);
-        if (s.bad && pass == 0 && blockIdx.x == 0) raise_bad();
+        s = load_seq(p.lens, p.cu, b, p.n, p.max_q, p.max_len);
+        if (s.bad && pass == 1 && blockIdx.x == 0) raise_bad();
         for (int rt = 0; rt < p.row_tiles; ++rt) c += row_tile_span<R>(p, s, rt).count;
         c *= p.Hkv;
       }
-      long long x = c;
+      int x = c;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
-        const long long y = __shfl_up_sync(0xffffffffu, x, o);
+        const int y = __shfl_up_sync(0xffffffffu, x, o);
         if (lane >= o) x += y;
       }
-      __syncthreads();
+      __syncthreads();  // the last chunk's sums are read
       if (lane == 31) scan[warp] = x;
       __syncthreads();
-      long long before = base;
+      x += base;
 #pragma unroll
       for (int w = 0; w < kSplitWarps; ++w) {
-        if (w < warp) before += scan[w];
+        if (w < warp) x += scan[w];
         base += scan[w];
       }
-      x += before;  // tiles up to and with sequence b
-      if (pass == 1 || B <= kSplitThreads) {
+      // x: tiles up to and with sequence b
+      if (pass == 1) {
         if (B <= kSplitThreads) total = base;
-        const long long each = (total + gridDim.x - 1) / gridDim.x;
-        const int share = (int)((each + kSplitWarps - 1) / kSplitWarps * kSplitWarps);
+        const int each = (int)(((unsigned)total + gridDim.x - 1) / gridDim.x);
+        const int share = (each + kSplitWarps - 1) / kSplitWarps * kSplitWarps;
         const long long at = (long long)blockIdx.x * share;
-        if (threadIdx.x == 0 && b0 == 0) found = Share{at, at, 0, share, 0};
-        __syncthreads();
-        if (at >= x - c && at < x) found = Share{at, min(total, at + share), b, share, x - c};
+        if (at >= x - c && at < x) found = Share{(int)at, (int)min((long long)total, at + share), share, b, x - c, c, s};
       }
     }
     total = base;
-    if (B <= kSplitThreads) break;
   }
   __syncthreads();
   return found;
@@ -447,32 +448,34 @@ __global__ void __launch_bounds__(kSplitThreads, resident_ctas(D, NT)) split_ker
   constexpr int R = 8 * NT;
   extern __shared__ __align__(16) float sm[];
   const Share sh = find_share<R>(p, B);
-  long long at = sh.at, b_at = sh.b_at;
-  for (int b = sh.b; at < sh.end && b < B; ++b) {
-    const Seq s = load_seq(p.lens, p.cu, b, p.n, p.max_q, p.max_len);
-    int per_head = 0;  // tiles of one kv head
-    for (int rt = 0; rt < p.row_tiles; ++rt) per_head += row_tile_span<R>(p, s, rt).count;
-    const long long b_end = b_at + (long long)per_head * p.Hkv;
-    while (at < sh.end && at < b_end) {
-      const int hk = (int)((at - b_at) / per_head);
-      int v = (int)((at - b_at) % per_head), rt = 0;
+  int at = sh.at, b_at = sh.b_at, b_c = sh.b_c;
+  Seq s = sh.s;
+  for (int b = sh.b; at < sh.end;) {
+    const int per_head = b_c / p.Hkv;
+    while (at < sh.end && at < b_at + b_c) {
+      const int hk = (at - b_at) / per_head;
+      int v = (at - b_at) - hk * per_head, rt = 0;
       Span<kTile> span = row_tile_span<R>(p, s, 0);
       while (v >= span.count) {
         v -= span.count;
         span = row_tile_span<R>(p, s, ++rt);
       }
-      const int v1 = (int)min((long long)span.count, v + (sh.end - at));
+      const int v1 = min(span.count, v + (sh.end - at));
       const int unit = (b * p.Hkv + hk) * p.row_tiles + rt;
       const bool whole = v == 0 && v1 == span.count;
-      if (v == 0 && threadIdx.x == 0) {  // the unit's first slot and how many it has
-        const long long u_at = at, last = u_at + span.count - 1;
-        p.unit_slots[unit] = make_int2((int)blockIdx.x + unit, (int)(last / sh.share - u_at / sh.share) + 1);
-      }
+      if (v == 0 && threadIdx.x == 0)  // the unit's first slot and how many it has
+        p.unit_slots[unit] = make_int2((int)blockIdx.x + unit, (at + span.count - 1) / sh.share - (int)blockIdx.x + 1);
       split_segment<D, NT>(p, s, b, hk, rt, span, v, v1, whole ? -1 : (long long)blockIdx.x + unit, sm);
       at += v1 - v;
       __syncthreads();  // shared memory is free again
     }
-    b_at = b_end;
+    b_at += b_c;
+    if (at < sh.end) {
+      s = load_seq(p.lens, p.cu, ++b, p.n, p.max_q, p.max_len);
+      b_c = 0;
+      for (int rt = 0; rt < p.row_tiles; ++rt) b_c += row_tile_span<R>(p, s, rt).count;
+      b_c *= p.Hkv;
+    }
   }
 }
 
