@@ -27,7 +27,10 @@ constexpr float kPfLazy = 6.0f;  // a row's maximum is raised when exceeded by 2
 constexpr float kTiny = 1.17549435e-38f;  // a logit's scale is never 0: -inf times it stays -inf
 constexpr float kPfShift = 9.0f; // P enters FP16 times 2^9: at most 2^15
 
-enum PfBar : int { KFULL = 0, KEMPTY = 2, VFULL = 4, VEMPTY = 6, SFULL = 8, PFULL = 10, PVDONE = 12, DRAIN = 14, NPFBAR = 15 };
+enum PfBar : int {
+  KFULL = 0, KEMPTY = 2, VFULL = 4, VEMPTY = 6, SFULL = 8,
+  PFULL = 10,  // [half of the tokens][row tile]
+  PVDONE = 14, DRAIN = 16, NPFBAR = 17 };
 
 template <int D>
 struct PfLayout {
@@ -56,6 +59,9 @@ __device__ __forceinline__ uint32_t hmul2_u32(uint32_t a, __half2 m) {
   const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&a), m);
   return *reinterpret_cast<const uint32_t*>(&r);
 }
+
+// The lowest n bits (n may be negative or above 32).
+__device__ __forceinline__ uint32_t bits_below(int n) { return n <= 0 ? 0u : n >= 32 ? 0xFFFFFFFFu : (1u << n) - 1u; }
 
 __device__ __forceinline__ void pf_raise(volatile int* abort) {
   *abort = 1;
@@ -99,7 +105,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const AttnParams
   int* eref = reinterpret_cast<int*>(smem + L::OFF_MISC + 12);
   if (tid == 0) {
     for (int k = 0; k < NPFBAR; ++k)
-      mbar_init(BAR(k), (k >= KFULL && k < KFULL + 2) || (k >= VFULL && k < VFULL + 2) || (k >= PFULL && k < PFULL + 2) ? 4 : 1);
+      mbar_init(BAR(k), (k >= KFULL && k < KFULL + 2) || (k >= VFULL && k < VFULL + 2) || (k >= PFULL && k < PFULL + 4) ? 4 : 1);
     *abort = 0;
     misc[2] = 0;
     eref[0] = eref[1] = 0;
@@ -207,26 +213,24 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const AttnParams
       }
       for (int j = 0; ok && j < nj; ++j) {
         const int st = j & 1, sn = st ^ 1;
-        for (int t = 0; t < ntile; ++t) {
-          if (!wait(PFULL + t, j & 1) || (t == 0 && !wait(VFULL + st, (j >> 1) & 1))) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
+        // operands first: once a tile's P is there, its products go out without another wait
+        if (!wait(VFULL + st, (j >> 1) & 1) || (j + 1 < nj && !wait(KFULL + sn, ((j + 1) >> 1) & 1))) ok = false;
+        for (int t = 0; ok && t < ntile; ++t) {
 #pragma unroll
-          for (int k = 0; k < 8; ++k)  // 16 tokens a step: 16 rows of 128 bytes
-            mma_f16_ts_el(el, tm + L::O_COL + D * t, tm + L::S_COL + 128 * t + 8 * k, v_lo + st * TSTEP + 128 * k, HI,
-                          idesc_f16(D, 1), (j > 0 || k > 0) ? 1u : 0u);
-          tc_commit_el(el, BAR(PVDONE + t));
-          if (j + 1 < nj) {
-            if (t == 0 && !wait(KFULL + sn, ((j + 1) >> 1) & 1)) {
-              ok = false;
-              break;
-            }
+          for (int half = 0; half < 2; ++half) {
+            ok = ok && wait(PFULL + 2 * half + t, j & 1);
+            if (!ok) break;
             tc_fence_after();
-            qk(t, sn);
+#pragma unroll
+            for (int k = 4 * half; k < 4 * half + 4; ++k)  // 16 tokens a step: 16 rows of 128 bytes
+              mma_f16_ts_el(el, tm + L::O_COL + D * t, tm + L::S_COL + 128 * t + 8 * k, v_lo + st * TSTEP + 128 * k, HI,
+                            idesc_f16(D, 1), (j > 0 || k > 0) ? 1u : 0u);
           }
+          if (!ok) break;
+          tc_commit_el(el, BAR(PVDONE + t));
+          if (j + 1 < nj) qk(t, sn);
         }
+        if (!ok) break;
         tc_commit_el(el, BAR(VEMPTY + st));
         if (j + 1 < nj) tc_commit_el(el, BAR(KEMPTY + sn));
       }
@@ -343,55 +347,60 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const AttnParams
       const bool bad_pages = misc[2] != 0;
       const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
       const uint32_t s_addr = lane_base + L::S_COL + 128 * tile, o_addr = lane_base + L::O_COL + D * tile;
+      const bool idle = tile * 128 + (warp & 3) * 32 >= r_cnt;
       float m_ref = -INFINITY, l = 0.0f;
       bool ok = true;
       for (int j = 0; j < nj; ++j) {
         if (!__all_sync(0xffffffffu, mbar_wait(BAR(SFULL + tile), j & 1, abort, kPfWaitNs))) { ok = false; break; }
         tc_fence_after();
-        uint32_t v[128];
-#pragma unroll
-        for (int c4 = 0; c4 < 4; ++c4) tmem_ld32(s_addr + 32 * c4, *reinterpret_cast<uint32_t(*)[32]>(&v[32 * c4]));
-        tmem_ld_wait();
+        if (idle) {  // no row of this warp is one of the call's
+          if (lane == 0) {
+            mbar_arrive(BAR(PFULL + tile));
+            mbar_arrive(BAR(PFULL + 2 + tile));
+          }
+          continue;
+        }
+        uint32_t v[4][32];
+        tmem_ld32(s_addr, v[0]);
         const int tok = span.token(v0 + j);
-        if (bad_pages || !all_visible(p, tok, kPrefillTile, t_lo, t_hi)) {
+        const bool edge = bad_pages || !all_visible(p, tok, kPrefillTile, t_lo, t_hi);
+        uint32_t see[4] = {0, 0, 0, 0};
+        if (edge) {
           // columns [lo, hi] are in sight, and those below `sk`
           const int hi = pos - tok, lo = p.window > 0 ? pos - p.window + 1 - tok : 0;
-          const int sk = min(p.sinks - tok, hi + 1);
+          const int sk = p.window > 0 ? min(p.sinks - tok, hi + 1) : 0;
 #pragma unroll
-          for (int c = 0; c < 128; ++c)
-            if (!((c >= lo && c <= hi) || (p.window > 0 && c < sk))) v[c] = __float_as_uint(-INFINITY);
-          if (bad_pages) {
+          for (int c4 = 0; c4 < 4; ++c4)
+            see[c4] = (bits_below(hi + 1 - 32 * c4) & ~bits_below(lo - 32 * c4)) | bits_below(sk - 32 * c4);
+          if (bad_pages) {  // tokens of pages that are not of the pool
             for (int g = 0; g < 8; ++g) {
               const int tg = tok + 16 * g;
-              bool gone = false;
-              if (any_visible(p, tg, 16, p_lo, p_hi)) {
-                const int pg = __ldg(trow + (tg >> p.page_log2));
-                gone = pg < 0 || pg >= p.num_pages;
-              }
-              if (gone) {
-#pragma unroll
-                for (int c = 0; c < 128; ++c)
-                  if ((c >> 4) == g) v[c] = __float_as_uint(-INFINITY);
-              }
+              if (!any_visible(p, tg, 16, p_lo, p_hi)) continue;
+              const int pg = __ldg(trow + (tg >> p.page_log2));
+              if (pg < 0 || pg >= p.num_pages) see[g >> 1] &= ~(0xFFFFu << (16 * (g & 1)));
             }
           }
         }
-        float mloc;
-        {
-          float t1[43];
+        // the row's maximum, 32 columns at a time while the next are on their way
+        float mc[4];
 #pragma unroll
-          for (int c = 0; c < 42; ++c)
-            t1[c] = fmax3(__uint_as_float(v[3 * c]), __uint_as_float(v[3 * c + 1]), __uint_as_float(v[3 * c + 2]));
-          t1[42] = fmaxf(__uint_as_float(v[126]), __uint_as_float(v[127]));
-          float t2[15];
+        for (int c4 = 0; c4 < 4; ++c4) {
+          tmem_ld_wait32(v[c4]);
+          if (c4 < 3) tmem_ld32(s_addr + 32 * (c4 + 1), v[c4 + 1]);
+          if (edge) {
 #pragma unroll
-          for (int c = 0; c < 14; ++c) t2[c] = fmax3(t1[3 * c], t1[3 * c + 1], t1[3 * c + 2]);
-          t2[14] = t1[42];
-          float t3[5];
+            for (int c = 0; c < 32; ++c)
+              if (!(see[c4] & (1u << c))) v[c4][c] = __float_as_uint(-INFINITY);
+          }
+          float t1[11];
 #pragma unroll
-          for (int c = 0; c < 5; ++c) t3[c] = fmax3(t2[3 * c], t2[3 * c + 1], t2[3 * c + 2]);
-          mloc = fmaxf(fmax3(t3[0], t3[1], t3[2]), fmaxf(t3[3], t3[4])) * sc;
+          for (int c = 0; c < 10; ++c)
+            t1[c] = fmax3(__uint_as_float(v[c4][3 * c]), __uint_as_float(v[c4][3 * c + 1]), __uint_as_float(v[c4][3 * c + 2]));
+          t1[10] = fmaxf(__uint_as_float(v[c4][30]), __uint_as_float(v[c4][31]));
+          mc[c4] = fmax3(fmax3(t1[0], t1[1], t1[2]), fmax3(t1[3], t1[4], t1[5]),
+                         fmax3(fmax3(t1[6], t1[7], t1[8]), t1[9], t1[10]));
         }
+        const float mloc = fmaxf(fmaxf(mc[0], mc[1]), fmaxf(mc[2], mc[3])) * sc;
         float alpha = 1.0f;
         const bool grow = mloc > m_ref + kPfLazy;
         if (__any_sync(0xffffffffu, grow)) {
@@ -421,8 +430,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const AttnParams
           uint32_t pk[16];
 #pragma unroll
           for (int t = 0; t < 16; ++t) {
-            const int i = 16 * ch + t;
-            const uint64_t y = ffma2(f2pack(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])), sc2, nb2);
+            const uint64_t y = ffma2(f2pack(__uint_as_float(v[ch][2 * t]), __uint_as_float(v[ch][2 * t + 1])), sc2, nb2);
             float a0, a1;
             f2unpack(y, a0, a1);
             a0 = ex2_approx(a0);
@@ -432,15 +440,17 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const AttnParams
             pk[t] = *reinterpret_cast<const uint32_t*>(&h);
           }
           tmem_st16(s_addr + 16 * ch, pk);
+          if (ch & 1) {  // half of the tokens: their part of O += P V may start
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(BAR(PFULL + ch - 1 + tile));
+          }
         }
         float x0, x1, x2, x3;
         f2unpack(fadd2(acc[0], acc[1]), x0, x1);
         f2unpack(fadd2(acc[2], acc[3]), x2, x3);
         l += (x0 + x1) + (x2 + x3);
-        tmem_st_wait();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(BAR(PFULL + tile));
       }
       ok = ok && __all_sync(0xffffffffu, mbar_wait(BAR(PVDONE + tile), (nj - 1) & 1, abort, kPfWaitNs));
       if (!ok) {
