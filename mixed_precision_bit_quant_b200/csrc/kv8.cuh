@@ -53,7 +53,7 @@ __device__ __forceinline__ Seq load_seq(const int32_t* lens, const int32_t* cu, 
   return s;
 }
 
-// 16-byte and 8-byte loads of read-only data that stay where they are written: an ordinary
+// Loads of read-only data that stay where they are written: an ordinary
 // load may be moved down to its first use, past the wait that it is meant to overlap.
 __device__ __forceinline__ uint4 ldg16_now(const void* a) {
   uint4 u;
@@ -64,6 +64,11 @@ __device__ __forceinline__ uint2 ldg8_now(const void* a) {
   uint2 u;
   asm volatile("ld.global.nc.v2.u32 {%0,%1}, [%2];" : "=r"(u.x), "=r"(u.y) : "l"(a));
   return u;
+}
+__device__ __forceinline__ float ldg4_now(const float* a) {
+  float x;
+  asm volatile("ld.global.nc.f32 %0, [%1];" : "=f"(x) : "l"(a));
+  return x;
 }
 
 // Two e4m3 codes (low byte first) -> f16x2, exact.

@@ -11,7 +11,8 @@
 //                  state (maximum, sum, unnormalised output) where several CTAs share a tile
 //   prefill_kernel (kv8_prefill.cu) many rows
 //   merge_kernel   joins the runs' states of a row
-//   weights_kernel adds the rows' final weights to the running sums of the tokens
+//   logit_weights_kernel, tile_weights_kernel (kv8_prefill.cu)  add the rows' final weights to
+//                  the running sums of the tokens
 #include "kv8_attn.cuh"
 
 namespace thrift {
@@ -217,6 +218,7 @@ __device__ __forceinline__ void split_segment(const AttnParams& p, const Seq& s,
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int r_base = rt * R, r_cnt = min(s.nq * p.G - r_base, R);
   const int p_lo = s.pos0 + r_base / p.G, p_hi = s.pos0 + (r_base + r_cnt - 1) / p.G;
+  float* logit_row = p.logits + (((long long)b * p.Hkv + hk) * p.row_tiles + rt) * p.logit_tokens * p.logit_w;
   float* so = sm;                              // [warps][R][D + 4]
   float* sml = sm + kSplitWarps * R * (D + 4);  // [warps][R][2]
 
@@ -304,6 +306,15 @@ __device__ __forceinline__ void split_segment(const AttnParams& p, const Seq& s,
           for (int y = 0; y < D / 32; ++y) c.v[r][y] = 0u;
         }
       }
+    }
+    if (p.logits != nullptr) {
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+        if (8 * n + 2 * t < p.logit_w) {
+          float* at = logit_row + (long long)(tok + g) * p.logit_w + 8 * n + 2 * t;
+          *reinterpret_cast<float2*>(at) = make_float2(x[n][0], x[n][1]);
+          *reinterpret_cast<float2*>(at + 8 * p.logit_w) = make_float2(x[n][2], x[n][3]);
+        }
     }
     bool raise = false;
 #pragma unroll
@@ -570,57 +581,48 @@ __global__ void __launch_bounds__(32 * kMergeWarps) merge_kernel(const AttnParam
   }
 }
 
-// One warp per 16 tokens, over all rows that see them: the logits again, now with the rows'
-// final log-sum-exp, and their weights summed per token.  A token's sum is made by
-// one warp in a fixed order, so it does not depend on how the work is spread.
-template <int D>
-__global__ void __launch_bounds__(128) weights_kernel(const AttnParams p) {
+// The weight sums of few rows: split_kernel left every visible logit (log2 domain, FP32), and
+// a thread adds up one token's rows with their final log-sum-exp.  Storing the logits costs
+// 8 bytes a row and token, a fraction of the token's 2 D bytes of codes (4 rows and D = 128:
+// 1/8); computing them again took as long as the attention itself (75 us of 142 at 32
+// sequences of up to 8191 tokens, against 9).  One thread adds a token's rows in order: the sum does
+// not depend on how the work was spread.
+constexpr int kWeightRows = 64;  // the most rows of split_kernel
+__global__ void __launch_bounds__(256) logit_weights_kernel(const AttnParams p, int R) {
+  __shared__ float lse2[kWeightRows];
+  __shared__ int pos[kWeightRows];
   const int bk = blockIdx.y, b = bk / p.Hkv, hk = bk % p.Hkv;
-  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const Seq s = load_seq(p.lens, p.cu, b, p.n, p.max_q, p.max_len);
-  const int tok = (blockIdx.x * 4 + (threadIdx.x >> 5)) * kTile;
-  if (tok >= s.len || s.nq == 0) return;
-  // rows of the tokens: positions from tok on, up to the window's end unless they are sinks
-  const int i0 = max(0, tok - s.pos0);
-  int i1 = s.nq;
-  if (p.window > 0 && tok >= p.sinks) i1 = min(i1, tok + kTile - 1 + p.window - s.pos0);
-  if (i0 >= i1) return;
+  const int rows = s.nq * p.G, t0 = blockIdx.x * 256, tok = t0 + threadIdx.x;
+  if (t0 >= s.len || rows == 0) return;
+  if ((int)threadIdx.x < rows) {
+    lse2[threadIdx.x] = p.lse2[packed_row(p, s, hk, threadIdx.x)];
+    pos[threadIdx.x] = s.pos0 + threadIdx.x / p.G;
+  }
+  __syncthreads();
+  if (tok >= s.len || !any_visible(p, tok, 1, max(s.pos0, 0), s.len - 1)) return;
   const int pg = __ldg(p.table + (long long)b * p.table_cols + (tok >> p.page_log2));
-  if (pg < 0 || pg >= p.num_pages) return;  // reported by the attention
-  const long long ph = (long long)pg * p.Hkv + hk;
-  uint4 k[2][D / 64];
-  load_k<D>(p.k + (ph << p.page_log2) * D + (tok & ((1 << p.page_log2) - 1)) * D, g, t, k);
-  const float kscale = scale_value(__ldg(p.ks + ph));
-  float sum[2] = {0.0f, 0.0f};
-  for (int r0 = i0 * p.G; r0 < i1 * p.G; r0 += 8) {
-    uint32_t qf[1][D / 16][2];
-    const int r = r0 + g;
-    const int e = load_query<D>(r < s.nq * p.G ? query_row(p, s, hk, r, D) : nullptr, t, p.fp16, qf[0]);
-    float x[1][4];
-    tile_logits<D, 1>(k, qf, x);
+  if (pg < 0 || pg >= p.num_pages) return;  // no logits were left; reported by split_kernel
+  // a logit that its row does not see may be unwritten: it is loaded (no branch, so that the
+  // loads go out together) and dropped
+  const float w = p.w[(long long)bk * p.w_cols + tok];
+  const float* at = p.logits + ((long long)bk * p.row_tiles * p.logit_tokens + tok) * p.logit_w;
+  float sum = 0.0f;
+  for (int r0 = 0; r0 < rows; r0 += R, at += (long long)p.logit_tokens * p.logit_w) {
+#pragma unroll 4
+    for (int c = 0; c < min(R, rows - r0); c += 2) {
+      const float2 x = *reinterpret_cast<const float2*>(at + c);
 #pragma unroll
-    for (int y = 0; y < 2; ++y) {
-      const float f = pow2f(__shfl_sync(0xffffffffu, e, 4 * (2 * t + y))) * p.scale_log2;
-      const int c = r0 + 2 * t + y;
-      if (c < s.nq * p.G) {
-        const float lse2 = p.lse2[packed_row(p, s, hk, c)];
-        const int pp = s.pos0 + c / p.G;
-#pragma unroll
-        for (int z = 0; z < 2; ++z) {
-          const int tt = tok + g + 8 * z;
-          const bool see = tt <= pp && (p.window == 0 || tt > pp - p.window || tt < p.sinks);
-          if (see) sum[z] += ex2_approx(x[0][y + 2 * z] * (f * kscale) - lse2);
-        }
+      for (int y = 0; y < 2; ++y) {
+        const int r = r0 + c + y;
+        if (r >= rows) break;
+        const int pp = pos[r];
+        const bool see = tok <= pp && (p.window == 0 || tok > pp - p.window || tok < p.sinks);
+        sum += see ? ex2_approx((y ? x.y : x.x) - lse2[r]) : 0.0f;
       }
     }
   }
-#pragma unroll
-  for (int z = 0; z < 2; ++z) {
-    sum[z] += __shfl_xor_sync(0xffffffffu, sum[z], 1);
-    sum[z] += __shfl_xor_sync(0xffffffffu, sum[z], 2);
-    const int tt = tok + g + 8 * z;
-    if (t == 0 && tt < s.len) p.w[(long long)bk * p.w_cols + tt] += sum[z];
-  }
+  p.w[(long long)bk * p.w_cols + tok] = w + sum;
 }
 
 static Plan make_plan(const thrift_kv8_shape& s, const thrift_kv8_mask& m, bool with_w) {
@@ -661,6 +663,14 @@ static Plan make_plan(const thrift_kv8_shape& s, const thrift_kv8_mask& m, bool 
   p.o_off = take(states * s.d * sizeof(float));
   p.slots_off = take(p.tiles128 ? 0 : (size_t)units * sizeof(int2));
   p.lse_off = take(with_w ? nrow * sizeof(float) : 0);
+  const long long even = (rows + 1) / 2 * 2;
+  p.logit_w = (int)(even < R ? even : R);
+  p.logit_tokens = (s.max_len + kTile - 1) / kTile * kTile;
+  // prefill_kernel's query tiles for tile_weights_kernel
+  const size_t tiles128 = with_w && p.tiles128 ? (size_t)units * 2 : 0;
+  p.image_off = take(tiles128 * 128 * s.d * 2);
+  p.scale_off = take(tiles128 * 128 * sizeof(float));
+  p.logits_off = take(with_w && !p.tiles128 ? sizeof(float) * units * p.logit_tokens * p.logit_w : 0);
   p.bytes = at;
   return p;
 }
@@ -692,7 +702,7 @@ static cudaError_t launch_attn_d(const AttnParams& p, const Plan& plan, const th
     if (e != cudaSuccess) return e;
     ++launches;
   } else if (p.w != nullptr) {
-    weights_kernel<D><<<dim3((s.max_len + 4 * kTile - 1) / (4 * kTile), s.B * s.Hkv), 128, 0, st>>>(p);
+    logit_weights_kernel<<<dim3((s.max_len + 255) / 256, s.B * s.Hkv), 256, 0, st>>>(p, 8 * plan.nt);
     ++launches;
   }
   count_launches(launches);
@@ -720,6 +730,10 @@ cudaError_t launch_kv8_attn(const Kv8Args& a, const Kv8Attn& t, cudaStream_t st)
   p.unit_slots = reinterpret_cast<int2*>(ws + plan.slots_off);
   p.w = t.w; p.w_cols = t.w_cols;
   p.lse2 = t.w != nullptr ? reinterpret_cast<float*>(ws + plan.lse_off) : nullptr;
+  p.logits = t.w != nullptr && !plan.tiles128 ? reinterpret_cast<float*>(ws + plan.logits_off) : nullptr;
+  p.q_image = t.w != nullptr && plan.tiles128 ? ws + plan.image_off : nullptr;
+  p.q_scale = reinterpret_cast<float*>(ws + plan.scale_off);
+  p.logit_w = plan.logit_w; p.logit_tokens = plan.logit_tokens;
   p.Hq = a.s.Hq; p.Hkv = a.s.Hkv; p.G = a.s.Hq / a.s.Hkv;
   p.page_log2 = 31 - __builtin_clz((unsigned)a.s.page);
   p.table_cols = a.s.table_cols; p.n = a.s.n; p.max_q = a.s.max_q; p.max_len = a.s.max_len;

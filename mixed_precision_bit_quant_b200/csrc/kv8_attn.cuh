@@ -20,6 +20,10 @@ struct AttnParams {
   float* part_o;
   int2* unit_slots;  // split_kernel: first slot and slots of a (sequence, kv head, row tile)
   float* lse2;      // [row] log2-domain log-sum-exp for the weights (or null)
+  float* logits;    // split_kernel's logits for the weight sums, [sequence, kv head, row tile][token][logit_w] (or null)
+  uint8_t* q_image;  // prefill_kernel's query tiles and rows' scales for the weight sums (or null)
+  float* q_scale;
+  int logit_w, logit_tokens;
   float* w;
   long long w_cols;
   int Hq, Hkv, G, page_log2, table_cols, n, max_q, max_len, num_pages, window, sinks, fp16;
@@ -78,7 +82,8 @@ __device__ __forceinline__ bool all_visible(const AttnParams& p, int a, int n, i
 struct Plan {
   bool tiles128;  // prefill_kernel (128-row tiles) instead of split_kernel
   int nt, row_tiles, nsplit, chunk, ctas;
-  size_t ml_off, o_off, slots_off, lse_off, bytes;
+  size_t ml_off, o_off, slots_off, lse_off, logits_off, image_off, scale_off, bytes;
+  int logit_w, logit_tokens;
 };
 
 cudaError_t launch_prefill(const AttnParams& p, const thrift_kv8_shape& s, cudaStream_t st);

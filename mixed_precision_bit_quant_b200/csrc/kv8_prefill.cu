@@ -184,6 +184,13 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const AttnParams
   tc_fence_after();
   const uint32_t tmem = misc[0];
   const int kref = eref[0], vref = eref[1];
+  if (p.q_image != nullptr && split == 0) {  // for tile_weights_kernel, as they lie here
+    const long long at = ((long long)bk * p.row_tiles + rt) * 2;
+    uint4* dst = reinterpret_cast<uint4*>(p.q_image + at * L::TILE);
+    const uint4* src = reinterpret_cast<const uint4*>(smem + L::OFF_Q);
+    for (int i = tid; i < ntile * L::TILE / 16; i += kPfThreads) dst[i] = src[i];
+    if (warp < 8 && tile < ntile) p.q_scale[at * 128 + tile * 128 + row] = qscale;
+  }
   volatile int never = 0;
 
   if (warp >= 12) {
@@ -508,27 +515,31 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const AttnParams
 // that see them: S^T = K Q^T puts a token on a TMEM lane, so a token's sum over rows
 // is a thread's sum over columns -- no exchange, and in a fixed order.
 //   warps 0-3, 4-7  the even and the odd row tiles' exponentials and sums
-//   warps 8-11 query rows to FP16 in shared memory (one thread a row), with the row's
-//              scale and log-sum-exp
-//   warp 12    tensor-memory allocator and issuer
+//   warp 8     brings the row tiles' FP16 images, which prefill_kernel left in the workspace,
+//              by bulk copies, and the rows' scales and log-sum-exps
+//   warp 9     tensor-memory allocator and issuer
+// Two CTAs an SM: the exponentials of one run under the other's waits.  Making the images here,
+// once per token tile, took 368 us where this takes TWUS (2 x 1024 new tokens of 4096, 32 heads).
 // ---------------------------------------------------------------------------
-enum TwBar : int { QFULL = 0, QEMPTY = 3, WFULL = 6, WEMPTY = 8, WDRAIN = 10, NTWBAR = 11 };
-constexpr int kTwStages = 3, kTwThreads = 416;
+// The rows' numbers lie in six slots: when warp 8 fills tile j's, product j - 2 has completed,
+// so S of tile j - 4 was read and tile j - 6, the slot's last, is done with.
+constexpr int kTwStages = 2, kTwRowSlots = 6, kTwThreads = 320;
+enum TwBar : int { QFULL = 0, QEMPTY = 2, WFULL = 4, WEMPTY = 6, WDRAIN = 8, ROWS = 9, NTWBAR = ROWS + kTwRowSlots };
 
 template <int D>
 struct TwLayout {
   static constexpr int TILE = 128 * D * 2;
   static constexpr int OFF_K = 0;
   static constexpr int OFF_Q = TILE;                        // kTwStages row tiles
-  static constexpr int OFF_ROW = OFF_Q + kTwStages * TILE;  // [stage][64] of two rows' scale, scale, -lse, -lse
-  static constexpr int OFF_SUM = OFF_ROW + kTwStages * 1024;  // [128] the odd tiles' sums
+  static constexpr int OFF_ROW = OFF_Q + kTwStages * TILE;  // [slot][64] of two rows' scale, scale, -lse, -lse
+  static constexpr int OFF_SUM = OFF_ROW + kTwRowSlots * 1024;  // [128] the odd tiles' sums
   static constexpr int OFF_BAR = OFF_SUM + 512;
   static constexpr int OFF_MISC = OFF_BAR + 8 * NTWBAR + 8;
   static constexpr int DYN = OFF_MISC + 32 + 1024;
 };
 
 template <int D>
-__global__ void __launch_bounds__(kTwThreads, 1) tile_weights_kernel(const AttnParams p) {
+__global__ void __launch_bounds__(kTwThreads, 2) tile_weights_kernel(const AttnParams p) {
   using L = TwLayout<D>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -549,14 +560,12 @@ __global__ void __launch_bounds__(kTwThreads, 1) tile_weights_kernel(const AttnP
   volatile int* abort = reinterpret_cast<volatile int*>(smem + L::OFF_MISC + 4);
   int* eref = reinterpret_cast<int*>(smem + L::OFF_MISC + 8);
   if (tid == 0) {
-    // a stage is free once its product completed and the four warps that read its rows' numbers did
-    for (int k = 0; k < NTWBAR; ++k)
-      mbar_init(BAR(k), k < QEMPTY ? 4 : k < WFULL ? 5 : (k >= WEMPTY && k < WDRAIN) ? 4 : 1);
+    for (int k = 0; k < NTWBAR; ++k) mbar_init(BAR(k), k >= WEMPTY && k < WDRAIN ? 4 : 1);
     *abort = 0;
     *eref = 0;
     fence_mbar_init();
   }
-  if (warp == 12) {
+  if (warp == 9) {
     tmem_alloc(smem_u32(smem + L::OFF_MISC), 256);
     tmem_relinquish();
   }
@@ -611,86 +620,87 @@ __global__ void __launch_bounds__(kTwThreads, 1) tile_weights_kernel(const AttnP
   float sum = 0.0f;
   bool ok = true;
 
-  if (warp == 12) {
-    if (lane == 0) {
-      for (int j = 0; j < nt; ++j) {
-        const int st = j % kTwStages, buf = j & 1;
-        if (!mbar_wait(BAR(QFULL + st), (j / kTwStages) & 1, abort, kPfWaitNs) ||
-            (j >= 2 && !mbar_wait(BAR(WEMPTY + buf), ((j >> 1) - 1) & 1, abort, kPfWaitNs))) {
-          pf_raise(abort);
-          break;
-        }
-        tc_fence_after();
-#pragma unroll
-        for (int k = 0; k < D / 16; ++k) {
-          const uint32_t off = (k >> 2) * 16384 + (k & 3) * 32;
-          mma_bf16_ss(tmem + 128 * buf, smem_desc(sb + L::OFF_K + off, 16, 1024, SWZ_128B),
-                      smem_desc(sb + L::OFF_Q + st * L::TILE + off, 16, 1024, SWZ_128B), idesc_f16(128, 0), k > 0);
-        }
-        tc_commit(BAR(QEMPTY + st));
-        tc_commit(BAR(WFULL + buf));
-      }
-      tc_commit(BAR(WDRAIN));
-      mbar_wait(BAR(WDRAIN), 0, &never, kPfWaitNs);
-    }
-  } else if (warp >= 8) {
-    const int row = (warp - 8) * 32 + lane;
-    const float kf = pow2f(max(-126, kref - 127 - kUp)) * p.scale_log2;
+  if (warp == 9) {
+    const uint32_t el = elect_one(), tm = __shfl_sync(0xffffffffu, tmem, 0);
+    const uint32_t k_lo = desc_lo(sb + L::OFF_K, 16), q_lo = desc_lo(sb + L::OFF_Q, 16);
+    constexpr uint32_t HI = desc_hi(1024, SWZ_128B), TSTEP = L::TILE >> 4;
     for (int j = 0; j < nt; ++j) {
-      const int st = j % kTwStages, r = (rt0 + j) * 128 + row;
-      uint32_t q[D / 2];
-#pragma unroll
-      for (int c = 0; c < D / 8; ++c) {
-        uint4 x = make_uint4(0, 0, 0, 0);
-        if (r < rows) x = __ldg(reinterpret_cast<const uint4*>(query_row(p, s, hk, r, D)) + c);
-        q[4 * c] = x.x; q[4 * c + 1] = x.y; q[4 * c + 2] = x.z; q[4 * c + 3] = x.w;
+      const int st = j % kTwStages, buf = j & 1;
+      if (!__all_sync(0xffffffffu, mbar_wait(BAR(QFULL + st), (j / kTwStages) & 1, abort, kPfWaitNs) &&
+                                       (j < 2 || mbar_wait(BAR(WEMPTY + buf), ((j >> 1) - 1) & 1, abort, kPfWaitNs)))) {
+        if (lane == 0) pf_raise(abort);
+        break;
       }
-      const float lse2 = r < rows ? p.lse2[packed_row(p, s, hk, r)] : -INFINITY;
-      uint32_t am = 0;
+      tc_fence_after();
 #pragma unroll
-      for (int c = 0; c < D / 2; ++c) am = __vmaxu2(am, q[c] & 0x7FFF7FFFu);
-      am = max(am & 0xFFFFu, am >> 16);
-      const int e = max(-100, (int)(__float_as_uint(pair_to_float2(am, p.fp16).x) >> 23) - 127 - 14);
-      const float down = pow2f(-e);
+      for (int k = 0; k < D / 16; ++k) {
+        const uint32_t off = ((k >> 2) * 16384 + (k & 3) * 32) >> 4;
+        mma_f16_ss_el(el, tm + 128 * buf, k_lo + off, HI, q_lo + st * TSTEP + off, HI, idesc_f16(128, 0), k > 0);
+      }
+      tc_commit_el(el, BAR(QEMPTY + st));
+      tc_commit_el(el, BAR(WFULL + buf));
+    }
+    tc_commit_el(el, BAR(WDRAIN));
+    mbar_wait(BAR(WDRAIN), 0, &never, kPfWaitNs);
+  } else if (warp == 8) {
+    const float kf = pow2f(max(-126, kref - 127 - kUp));
+    const long long tile0 = (long long)bk * p.row_tiles * 2 + rt0;
+    int issued = 0;
+    float qs[4], lse2[4];
+    // loads without a branch (clamped to the last row): they are not waited for before use
+    auto fetch = [&](int j) {
+      const int jj = min(j, nt - 1);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int row = 4 * lane + i;
+        qs[i] = ldg4_now(p.q_scale + (tile0 + jj) * 128 + row);
+        lse2[i] = ldg4_now(p.lse2 + packed_row(p, s, hk, min((rt0 + jj) * 128 + row, rows - 1)));
+      }
+    };
+    fetch(0);
+    for (int j = 0; j < nt; ++j) {
+      const int st = j % kTwStages;
       if (j >= kTwStages && !__all_sync(0xffffffffu, mbar_wait(BAR(QEMPTY + st), (j / kTwStages - 1) & 1, abort, kPfWaitNs))) {
         ok = false;
         break;
       }
-#pragma unroll
-      for (int c = 0; c < D / 8; ++c) {
-        uint32_t h[4];
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          const float2 f = pair_to_float2(q[4 * c + x], p.fp16);
-          const __half2 hh = __floats2half2_rn(f.x * down, f.y * down);
-          h[x] = *reinterpret_cast<const uint32_t*>(&hh);
-        }
-        sts128(sb + L::OFF_Q + st * L::TILE + (c >> 3) * 16384 + row * 128 + (((c & 7) ^ (row & 7)) << 4),
-               make_uint4(h[0], h[1], h[2], h[3]));
+      if (lane == 0) {
+        mbar_expect_tx(BAR(QFULL + st), L::TILE);
+        bulk_load(sb + L::OFF_Q + st * L::TILE, p.q_image + (tile0 + j) * L::TILE, L::TILE, BAR(QFULL + st));
       }
+      issued = j + 1;
       // a row that sees nothing (lse = -inf) or is none gets -inf: its exponentials are 0
-      float* rp = reinterpret_cast<float*>(smem + L::OFF_ROW + st * 1024) + 4 * (row >> 1) + (row & 1);
-      rp[0] = fmaxf(pow2f(e) * kf, kTiny);
-      rp[2] = lse2 == -INFINITY ? -INFINITY : -lse2;
-      fence_proxy_async_smem();
+#pragma unroll
+      for (int i = 0; i < 4; ++i) lse2[i] = (rt0 + j) * 128 + 4 * lane + i < rows ? lse2[i] : -INFINITY;
+      float4* rp = reinterpret_cast<float4*>(smem + L::OFF_ROW + (j % kTwRowSlots) * 1024) + 2 * lane;
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        rp[i] = make_float4(fmaxf(qs[2 * i] * kf, kTiny), fmaxf(qs[2 * i + 1] * kf, kTiny),
+                            lse2[2 * i] == -INFINITY ? -INFINITY : -lse2[2 * i],
+                            lse2[2 * i + 1] == -INFINITY ? -INFINITY : -lse2[2 * i + 1]);
       __syncwarp();
-      if (lane == 0) mbar_arrive(BAR(QFULL + st));
+      if (lane == 0) mbar_arrive(BAR(ROWS + j % kTwRowSlots));
+      fetch(j + 1);
     }
-    if (!ok && lane == 0) pf_raise(abort);
+    if (!ok) {  // the copies in flight land before the CTA's shared memory goes away
+      if (lane == 0) pf_raise(abort);
+      for (int k = 0; k < kTwStages && k < issued; ++k) {
+        const int n = issued - 1 - k;
+        mbar_wait(BAR(QFULL + n % kTwStages), (n / kTwStages) & 1, &never, kPfWaitNs / 4);
+      }
+    }
   } else {
     const int grp = warp >> 2, tok = t0 + (warp & 3) * 32 + lane;
     const uint32_t base = tmem + ((uint32_t)((warp & 3) * 32) << 16) + 128 * grp;
     uint64_t acc[2] = {0, 0};
     for (int j = grp; j < nt; j += 2) {
-      const int st = j % kTwStages;
-      // the rows' numbers are written before QFULL, which the product waited for
       if (!__all_sync(0xffffffffu, mbar_wait(BAR(WFULL + grp), (j >> 1) & 1, abort, kPfWaitNs) &&
-                                       mbar_wait(BAR(QFULL + st), (j / kTwStages) & 1, abort, kPfWaitNs))) {
+                                       mbar_wait(BAR(ROWS + j % kTwRowSlots), (j / kTwRowSlots) & 1, abort, kPfWaitNs))) {
         ok = false;
         break;
       }
       tc_fence_after();
-      const float4* rp = reinterpret_cast<const float4*>(smem + L::OFF_ROW + st * 1024);
+      const float4* rp = reinterpret_cast<const float4*>(smem + L::OFF_ROW + (j % kTwRowSlots) * 1024);
       const int r0 = (rt0 + j) * 128;
       const bool edge = !all_visible(p, t0, 128, s.pos0 + r0 / p.G, s.pos0 + (min(rows, r0 + 128) - 1) / p.G);
 #pragma unroll
@@ -720,8 +730,6 @@ __global__ void __launch_bounds__(kTwThreads, 1) tile_weights_kernel(const AttnP
           acc[i & 1] = fadd2(acc[i & 1], f2pack(ex2_approx(a0), ex2_approx(a1)));
         }
       }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(BAR(QEMPTY + st));
     }
     if (!ok && lane == 0) pf_raise(abort);
     float a0, a1;
@@ -731,7 +739,7 @@ __global__ void __launch_bounds__(kTwThreads, 1) tile_weights_kernel(const AttnP
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 12) {
+  if (warp == 9) {
     tc_fence_after();
     tmem_dealloc(tmem, 256);
   }
