@@ -669,7 +669,7 @@ static Plan make_plan(const thrift_kv8_shape& s, const thrift_kv8_mask& m, bool 
   // prefill_kernel's query tiles for tile_weights_kernel
   const size_t tiles128 = with_w && p.tiles128 ? (size_t)units * 2 : 0;
   p.image_off = take(tiles128 * 128 * s.d * 2);
-  p.scale_off = take(tiles128 * 128 * sizeof(float));
+  p.scale_off = take(tiles128 * sizeof(float));
   p.logits_off = take(with_w && !p.tiles128 ? sizeof(float) * units * p.logit_tokens * p.logit_w : 0);
   p.bytes = at;
   return p;

@@ -19,7 +19,7 @@ namespace thrift {
 namespace kv8 {
 
 constexpr int kPfThreads = 512;
-constexpr int kPfSoftmaxRegs = 184, kPfConvRegs = 104, kPfOtherRegs = 40;
+constexpr int kPfSoftmaxRegs = 176, kPfConvRegs = 112, kPfOtherRegs = 48;
 static_assert(2 * kPfSoftmaxRegs + kPfConvRegs + kPfOtherRegs <= 512, "register split exceeds the launch budget");
 constexpr uint64_t kPfWaitNs = 2000000000ull;  // 2 s per wait: far above any legitimate wait
 constexpr int kUp = 6;          // codes enter FP16 times 2^6: at most 448 * 64 < 65504
@@ -39,7 +39,7 @@ struct PfLayout {
   static constexpr int OFF_K = 2 * TILE;      // two stages
   static constexpr int OFF_V = 4 * TILE;      // two stages
   static constexpr int OFF_BAR = 6 * TILE;
-  static constexpr int OFF_MISC = OFF_BAR + 8 * NPFBAR + 8;  // tmem holder, abort, bad page, e_ref of K, of V
+  static constexpr int OFF_MISC = OFF_BAR + 8 * NPFBAR + 8;  // tmem holder, abort, bad page, e_ref of K, of V, largest |q| of two tiles
   static constexpr int BYTES = OFF_MISC + 32;
   // at least 116 KB, so that one CTA (and its 512 TMEM columns) owns an SM
   static constexpr int DYN = (BYTES + 1024 > 116 * 1024) ? BYTES + 1024 : 116 * 1024;
@@ -103,12 +103,14 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const AttnParams
   volatile uint32_t* misc = reinterpret_cast<volatile uint32_t*>(smem + L::OFF_MISC);
   volatile int* abort = reinterpret_cast<volatile int*>(smem + L::OFF_MISC + 4);
   int* eref = reinterpret_cast<int*>(smem + L::OFF_MISC + 12);
+  uint32_t* qmax = reinterpret_cast<uint32_t*>(smem + L::OFF_MISC + 20);  // of a row tile, as bits
   if (tid == 0) {
     for (int k = 0; k < NPFBAR; ++k)
       mbar_init(BAR(k), (k >= KFULL && k < KFULL + 2) || (k >= VFULL && k < VFULL + 2) || (k >= PFULL && k < PFULL + 4) ? 4 : 1);
     *abort = 0;
     misc[2] = 0;
     eref[0] = eref[1] = 0;
+    qmax[0] = qmax[1] = 0;
     fence_mbar_init();
   }
   if (warp == 12) {
@@ -145,13 +147,15 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const AttnParams
       raise_bad();
     }
   }
-  // a softmax thread's query row: FP16, scaled by a power of two, to shared memory
-  float qscale = 0.0f;
+  // A softmax thread's query row: FP16, scaled by a power of two, to shared memory.  The 128 rows
+  // of a tile share it (their largest component lands in [2^14, 2^15)), so that a logit's scale
+  // is the tile's: a component 2^31 (BF16) times below the tile's largest loses bits, and then
+  // at most 2^-39 of it -- logits are off by that much of the tile's largest possible one.
   const int tile = warp >> 2;  // of a softmax warp
   const int row = (warp & 3) * 32 + lane;
+  uint32_t q[D / 2];
   if (warp < 8 && tile < ntile) {
     const int r = tile * 128 + row;
-    uint32_t q[D / 2];
 #pragma unroll
     for (int c = 0; c < D / 8; ++c) {
       uint4 u = make_uint4(0, 0, 0, 0);
@@ -161,10 +165,17 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const AttnParams
     uint32_t am = 0;
 #pragma unroll
     for (int c = 0; c < D / 2; ++c) am = __vmaxu2(am, q[c] & 0x7FFF7FFFu);
-    am = max(am & 0xFFFFu, am >> 16);
-    const int e = max(-100, (int)(__float_as_uint(pair_to_float2(am, p.fp16).x) >> 23) - 127 - 14);
-    const float down = pow2f(-e);
-    qscale = pow2f(e) * p.scale_log2;
+    am = __reduce_max_sync(0xffffffffu, max(am & 0xFFFFu, am >> 16));
+    if (lane == 0) atomicMax(qmax + tile, am);
+  }
+  __syncthreads();
+  const float kscale = pow2f(max(-126, eref[0] - 127 - kUp));
+  float sc = 0.0f;  // of a logit
+  if (warp < 8 && tile < ntile) {
+    const int e = max(-100, (int)(__float_as_uint(pair_to_float2(qmax[tile], p.fp16).x) >> 23) - 127 - 14);
+    const float down = pow2f(-e), qscale = pow2f(e) * p.scale_log2;
+    sc = fmaxf(qscale * kscale, kTiny);
+    if (p.q_image != nullptr && split == 0 && row == 0) p.q_scale[((long long)bk * p.row_tiles + rt) * 2 + tile] = qscale;
 #pragma unroll
     for (int c = 0; c < D / 8; ++c) {
       uint32_t h[4];
@@ -189,7 +200,6 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const AttnParams
     uint4* dst = reinterpret_cast<uint4*>(p.q_image + at * L::TILE);
     const uint4* src = reinterpret_cast<const uint4*>(smem + L::OFF_Q);
     for (int i = tid; i < ntile * L::TILE / 16; i += kPfThreads) dst[i] = src[i];
-    if (warp < 8 && tile < ntile) p.q_scale[at * 128 + tile * 128 + row] = qscale;
   }
   volatile int never = 0;
 
@@ -350,7 +360,6 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const AttnParams
       const int pos = r < r_cnt ? s.pos0 + (r_base + r) / p.G : -1;
       const int t_lo = s.pos0 + (r_base + tile * 128) / p.G;
       const int t_hi = s.pos0 + (r_base + min(r_cnt, tile * 128 + 128) - 1) / p.G;
-      const float sc = fmaxf(qscale * pow2f(max(-126, kref - 127 - kUp)), kTiny);
       const bool bad_pages = misc[2] != 0;
       const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
       const uint32_t s_addr = lane_base + L::S_COL + 128 * tile, o_addr = lane_base + L::O_COL + D * tile;
@@ -531,8 +540,9 @@ struct TwLayout {
   static constexpr int TILE = 128 * D * 2;
   static constexpr int OFF_K = 0;
   static constexpr int OFF_Q = TILE;                        // kTwStages row tiles
-  static constexpr int OFF_ROW = OFF_Q + kTwStages * TILE;  // [slot][64] of two rows' scale, scale, -lse, -lse
-  static constexpr int OFF_SUM = OFF_ROW + kTwRowSlots * 1024;  // [128] the odd tiles' sums
+  static constexpr int OFF_ROW = OFF_Q + kTwStages * TILE;  // [slot] 128 rows' -lse, the tile's scale
+  static constexpr int ROW = 528;
+  static constexpr int OFF_SUM = OFF_ROW + kTwRowSlots * ROW;  // [128] the odd tiles' sums
   static constexpr int OFF_BAR = OFF_SUM + 512;
   static constexpr int OFF_MISC = OFF_BAR + 8 * NTWBAR + 8;
   static constexpr int DYN = OFF_MISC + 32 + 1024;
@@ -646,16 +656,13 @@ __global__ void __launch_bounds__(kTwThreads, 2) tile_weights_kernel(const AttnP
     const float kf = pow2f(max(-126, kref - 127 - kUp));
     const long long tile0 = (long long)bk * p.row_tiles * 2 + rt0;
     int issued = 0;
-    float qs[4], lse2[4];
+    float lse2[4], qs;
     // loads without a branch (clamped to the last row): they are not waited for before use
     auto fetch = [&](int j) {
       const int jj = min(j, nt - 1);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int row = 4 * lane + i;
-        qs[i] = ldg4_now(p.q_scale + (tile0 + jj) * 128 + row);
-        lse2[i] = ldg4_now(p.lse2 + packed_row(p, s, hk, min((rt0 + jj) * 128 + row, rows - 1)));
-      }
+      for (int i = 0; i < 4; ++i) lse2[i] = ldg4_now(p.lse2 + packed_row(p, s, hk, min((rt0 + jj) * 128 + 4 * lane + i, rows - 1)));
+      qs = ldg4_now(p.q_scale + tile0 + jj);
     };
     fetch(0);
     for (int j = 0; j < nt; ++j) {
@@ -671,13 +678,11 @@ __global__ void __launch_bounds__(kTwThreads, 2) tile_weights_kernel(const AttnP
       issued = j + 1;
       // a row that sees nothing (lse = -inf) or is none gets -inf: its exponentials are 0
 #pragma unroll
-      for (int i = 0; i < 4; ++i) lse2[i] = (rt0 + j) * 128 + 4 * lane + i < rows ? lse2[i] : -INFINITY;
-      float4* rp = reinterpret_cast<float4*>(smem + L::OFF_ROW + (j % kTwRowSlots) * 1024) + 2 * lane;
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-        rp[i] = make_float4(fmaxf(qs[2 * i] * kf, kTiny), fmaxf(qs[2 * i + 1] * kf, kTiny),
-                            lse2[2 * i] == -INFINITY ? -INFINITY : -lse2[2 * i],
-                            lse2[2 * i + 1] == -INFINITY ? -INFINITY : -lse2[2 * i + 1]);
+      for (int i = 0; i < 4; ++i)
+        lse2[i] = (rt0 + j) * 128 + 4 * lane + i >= rows || lse2[i] == -INFINITY ? -INFINITY : -lse2[i];
+      float* rp = reinterpret_cast<float*>(smem + L::OFF_ROW + (j % kTwRowSlots) * L::ROW);
+      reinterpret_cast<float4*>(rp)[lane] = make_float4(lse2[0], lse2[1], lse2[2], lse2[3]);
+      if (lane == 0) rp[128] = fmaxf(qs * kf, kTiny);
       __syncwarp();
       if (lane == 0) mbar_arrive(BAR(ROWS + j % kTwRowSlots));
       fetch(j + 1);
@@ -700,7 +705,9 @@ __global__ void __launch_bounds__(kTwThreads, 2) tile_weights_kernel(const AttnP
         break;
       }
       tc_fence_after();
-      const float4* rp = reinterpret_cast<const float4*>(smem + L::OFF_ROW + (j % kTwRowSlots) * 1024);
+      const float4* rp = reinterpret_cast<const float4*>(smem + L::OFF_ROW + (j % kTwRowSlots) * L::ROW);
+      const float sc = reinterpret_cast<const float*>(rp)[128];
+      const uint64_t sc2 = f2pack(sc, sc);
       const int r0 = (rt0 + j) * 128;
       const bool edge = !all_visible(p, t0, 128, s.pos0 + r0 / p.G, s.pos0 + (min(rows, r0 + 128) - 1) / p.G);
 #pragma unroll
@@ -722,12 +729,13 @@ __global__ void __launch_bounds__(kTwThreads, 2) tile_weights_kernel(const AttnP
           }
         }
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const float4 f = rp[16 * c4 + i];
-          const uint64_t y = ffma2(f2pack(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])), f2pack(f.x, f.y), f2pack(f.z, f.w));
+        for (int i = 0; i < 8; ++i) {
+          const float4 nl = rp[8 * c4 + i];
           float a0, a1;
-          f2unpack(y, a0, a1);
-          acc[i & 1] = fadd2(acc[i & 1], f2pack(ex2_approx(a0), ex2_approx(a1)));
+          f2unpack(ffma2(f2pack(__uint_as_float(v[4 * i]), __uint_as_float(v[4 * i + 1])), sc2, f2pack(nl.x, nl.y)), a0, a1);
+          acc[0] = fadd2(acc[0], f2pack(ex2_approx(a0), ex2_approx(a1)));
+          f2unpack(ffma2(f2pack(__uint_as_float(v[4 * i + 2]), __uint_as_float(v[4 * i + 3])), sc2, f2pack(nl.z, nl.w)), a0, a1);
+          acc[1] = fadd2(acc[1], f2pack(ex2_approx(a0), ex2_approx(a1)));
         }
       }
     }
