@@ -39,8 +39,8 @@ struct PfLayout {
   static constexpr int OFF_K = 2 * TILE;      // two stages
   static constexpr int OFF_V = 4 * TILE;      // two stages
   static constexpr int OFF_BAR = 6 * TILE;
-  static constexpr int OFF_MISC = OFF_BAR + 8 * NPFBAR + 8;  // tmem holder, abort, bad page, e_ref of K, of V, largest |q| of two tiles
-  static constexpr int BYTES = OFF_MISC + 32;
+  static constexpr int OFF_MISC = OFF_BAR + 8 * NPFBAR + 8;  // tmem holder, abort, 12 + 8 words of the start
+  static constexpr int BYTES = OFF_MISC + 96;
   // at least 116 KB, so that one CTA (and its 512 TMEM columns) owns an SM
   static constexpr int DYN = (BYTES + 1024 > 116 * 1024) ? BYTES + 1024 : 116 * 1024;
   static constexpr uint32_t S_COL = 0, O_COL = 256;  // S of tile t at 128 t (P over its first half), O at 256 + D t
@@ -102,30 +102,85 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const AttnParams
   auto BAR = [&](int k) -> uint32_t { return sb + L::OFF_BAR + 8 * k; };
   volatile uint32_t* misc = reinterpret_cast<volatile uint32_t*>(smem + L::OFF_MISC);
   volatile int* abort = reinterpret_cast<volatile int*>(smem + L::OFF_MISC + 4);
-  int* eref = reinterpret_cast<int*>(smem + L::OFF_MISC + 12);
-  uint32_t* qmax = reinterpret_cast<uint32_t*>(smem + L::OFF_MISC + 20);  // of a row tile, as bits
+  volatile uint32_t* ekey = misc + 2;  // of each of warps 12-15: largest exponents of K and of V, a bad page
+  volatile uint32_t* qkey = misc + 14;  // of each softmax warp: its largest |q|, as bits
   if (tid == 0) {
     for (int k = 0; k < NPFBAR; ++k)
       mbar_init(BAR(k), (k >= KFULL && k < KFULL + 2) || (k >= VFULL && k < VFULL + 2) || (k >= PFULL && k < PFULL + 4) ? 4 : 1);
     *abort = 0;
-    misc[2] = 0;
-    eref[0] = eref[1] = 0;
-    qmax[0] = qmax[1] = 0;
     fence_mbar_init();
   }
   if (warp == 12) {
     tmem_alloc(smem_u32(smem + L::OFF_MISC), 512);
     tmem_relinquish();
   }
-  __syncthreads();
   const int32_t* trow = p.table + (long long)b * p.table_cols;
   const int page_tok = 1 << p.page_log2;
-  // the largest exponents of the run's pages, and whether one is not of the pool
-  {
+  constexpr int LPR = D / 16, RPI = 32 / LPR;  // lanes per token, tokens per load of a warp
+  const int cw = warp - 8, c = lane % LPR, rr = lane / LPR;
+  // lane l of a batch: tile l / 2, group of 16 tokens 2 cw + (l & 1) of it
+  int l_page = -1, l_ks = 0, l_vs = 0;
+  auto batch = [&](int j0) {
+    const int j = j0 + (lane >> 1);
+    l_page = -1;
+    if (j < nj) {
+      const int tok = span.token(v0 + j) + 32 * cw + 16 * (lane & 1);
+      if (any_visible(p, tok, 16, p_lo, p_hi)) {
+        const int pg = __ldg(trow + (tok >> p.page_log2));
+        if (pg >= 0 && pg < p.num_pages) {
+          l_page = pg;
+          l_ks = __ldg(p.ks + (long long)pg * p.Hkv + hk);
+          l_vs = __ldg(p.vs + (long long)pg * p.Hkv + hk);
+        }
+      }
+    }
+  };
+  // Unconditional loads (a group that is not to be read takes page 0 and is zeroed below): a
+  // load under a branch would be waited for where the branches join.
+  auto load = [&](const uint8_t* base, int j, uint4 (&u)[LPR]) {
+    const int tok = span.token(v0 + j) + 32 * cw;
+#pragma unroll
+    for (int g = 0; g < 2; ++g) {
+      const int pg = max(0, __shfl_sync(0xffffffffu, l_page, 2 * (j & 15) + g));
+      const uint8_t* at = base + ((((long long)pg * p.Hkv + hk) << p.page_log2) + ((tok + 16 * g) & (page_tok - 1)) + rr) * D + 16 * c;
+#pragma unroll
+      for (int i = 0; i < LPR / 2; ++i) u[g * (LPR / 2) + i] = ldg16_now(at + i * RPI * D);
+    }
+  };
+  // The latencies of the start run side by side: the softmax warps load the query rows (whole
+  // rows at a time: one row a thread took 4096 wavefronts), the converters the first tile's
+  // codes, and the last four warps look through the run's pages.
+  const int tile = warp >> 2;  // of a softmax warp
+  const int row = (warp & 3) * 32 + lane;
+  constexpr int QV = D / 8;  // 16-byte vectors of a query row
+  uint4 uk[LPR], uv[LPR];    // converters: the next tile's codes; softmax warps: vectors 0 .. LPR - 1 and the rest of QV
+  if (warp < 8) {
+    if (tile < ntile) {
+#pragma unroll
+      for (int i = 0; i < QV; ++i) {
+        const int at = row + 128 * i, r = min(tile * 128 + at / QV, r_cnt - 1);
+        const uint4 u = ldg16_now(query_row(p, s, hk, r_base + r, D) + 4 * (at % QV));
+        if (i < LPR) uk[i % LPR] = u;
+        else uv[i % LPR] = u;
+      }
+      uint32_t am = 0;
+#pragma unroll
+      for (int i = 0; i < LPR; ++i) {
+        am = __vmaxu2(am, __vmaxu2(__vmaxu2(uk[i].x & 0x7FFF7FFFu, uk[i].y & 0x7FFF7FFFu), __vmaxu2(uk[i].z & 0x7FFF7FFFu, uk[i].w & 0x7FFF7FFFu)));
+        am = __vmaxu2(am, __vmaxu2(__vmaxu2(uv[i].x & 0x7FFF7FFFu, uv[i].y & 0x7FFF7FFFu), __vmaxu2(uv[i].z & 0x7FFF7FFFu, uv[i].w & 0x7FFF7FFFu)));
+      }
+      am = __reduce_max_sync(0xffffffffu, max(am & 0xFFFFu, am >> 16));
+      if (lane == 0) qkey[warp] = am;
+    }
+  } else if (warp < 12) {
+    batch(0);
+    load(p.k, 0, uk);
+    load(p.v, 0, uv);
+  } else {
     int ek = 0, ev = 0;
     bool bad = false;
     const int per = page_tok < kPrefillTile ? kPrefillTile >> p.page_log2 : 1;  // pages of a tile
-    for (int i = tid; i < nj * per; i += kPfThreads) {
+    for (int i = tid - 384; i < nj * per; i += 128) {
       const int tok = span.token(v0 + i / per) + (i % per) * page_tok;
       if (!any_visible(p, tok, page_tok, p_lo, p_hi)) continue;
       const int pg = __ldg(trow + (tok >> p.page_log2));
@@ -138,69 +193,57 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const AttnParams
     }
     ek = __reduce_max_sync(0xffffffffu, ek);
     ev = __reduce_max_sync(0xffffffffu, ev);
+    if (bad) raise_bad();
+    bad = __any_sync(0xffffffffu, bad);
     if (lane == 0) {
-      atomicMax(eref, ek);
-      atomicMax(eref + 1, ev);
+      ekey[warp - 12] = ek;
+      ekey[warp - 8] = ev;
+      ekey[warp - 4] = bad;
     }
-    if (bad) {
-      misc[2] = 1;
-      raise_bad();
-    }
-  }
-  // A softmax thread's query row: FP16, scaled by a power of two, to shared memory.  The 128 rows
-  // of a tile share it (their largest component lands in [2^14, 2^15)), so that a logit's scale
-  // is the tile's: a component 2^31 (BF16) times below the tile's largest loses bits, and then
-  // at most 2^-39 of it -- logits are off by that much of the tile's largest possible one.
-  const int tile = warp >> 2;  // of a softmax warp
-  const int row = (warp & 3) * 32 + lane;
-  uint32_t q[D / 2];
-  if (warp < 8 && tile < ntile) {
-    const int r = tile * 128 + row;
-#pragma unroll
-    for (int c = 0; c < D / 8; ++c) {
-      uint4 u = make_uint4(0, 0, 0, 0);
-      if (r < r_cnt) u = __ldg(reinterpret_cast<const uint4*>(query_row(p, s, hk, r_base + r, D)) + c);
-      q[4 * c] = u.x; q[4 * c + 1] = u.y; q[4 * c + 2] = u.z; q[4 * c + 3] = u.w;
-    }
-    uint32_t am = 0;
-#pragma unroll
-    for (int c = 0; c < D / 2; ++c) am = __vmaxu2(am, q[c] & 0x7FFF7FFFu);
-    am = __reduce_max_sync(0xffffffffu, max(am & 0xFFFFu, am >> 16));
-    if (lane == 0) atomicMax(qmax + tile, am);
-  }
-  __syncthreads();
-  const float kscale = pow2f(max(-126, eref[0] - 127 - kUp));
-  float sc = 0.0f;  // of a logit
-  if (warp < 8 && tile < ntile) {
-    const int e = max(-100, (int)(__float_as_uint(pair_to_float2(qmax[tile], p.fp16).x) >> 23) - 127 - 14);
-    const float down = pow2f(-e), qscale = pow2f(e) * p.scale_log2;
-    sc = fmaxf(qscale * kscale, kTiny);
-    if (p.q_image != nullptr && split == 0 && row == 0) p.q_scale[((long long)bk * p.row_tiles + rt) * 2 + tile] = qscale;
-#pragma unroll
-    for (int c = 0; c < D / 8; ++c) {
-      uint32_t h[4];
-#pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        const float2 f = pair_to_float2(q[4 * c + x], p.fp16);
-        const __half2 hh = __floats2half2_rn(f.x * down, f.y * down);
-        h[x] = *reinterpret_cast<const uint32_t*>(&hh);
-      }
-      sts128(sb + L::OFF_Q + tile * L::TILE + (c >> 3) * 16384 + row * 128 + (((c & 7) ^ (row & 7)) << 4),
-             make_uint4(h[0], h[1], h[2], h[3]));
-    }
-    fence_proxy_async_smem();
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = misc[0];
-  const int kref = eref[0], vref = eref[1];
-  if (p.q_image != nullptr && split == 0) {  // for tile_weights_kernel, as they lie here
-    const long long at = ((long long)bk * p.row_tiles + rt) * 2;
-    uint4* dst = reinterpret_cast<uint4*>(p.q_image + at * L::TILE);
-    const uint4* src = reinterpret_cast<const uint4*>(smem + L::OFF_Q);
-    for (int i = tid; i < ntile * L::TILE / 16; i += kPfThreads) dst[i] = src[i];
+  const int kref = max(max(ekey[0], ekey[1]), max(ekey[2], ekey[3]));
+  const int vref = max(max(ekey[4], ekey[5]), max(ekey[6], ekey[7]));
+  const bool bad_pages = (ekey[8] | ekey[9] | ekey[10] | ekey[11]) != 0;
+  // The rows as FP16, scaled by a power of two.  The 128 rows of a tile share it (their largest
+  // component lands in [2^14, 2^15)), so that a logit's scale is the tile's: a component 2^31
+  // (BF16) times below the tile's largest loses bits, and then at most 2^-39 of it -- logits
+  // are off by that much of the tile's largest possible one.
+  float sc = 0.0f;  // of a logit
+  if (warp < 8 && tile < ntile) {
+    const uint32_t am = max(max(qkey[4 * tile], qkey[4 * tile + 1]), max(qkey[4 * tile + 2], qkey[4 * tile + 3]));
+    const int e = max(-100, (int)(__float_as_uint(pair_to_float2(am, p.fp16).x) >> 23) - 127 - 14);
+    const float down = pow2f(-e), qscale = pow2f(e) * p.scale_log2;
+    sc = fmaxf(qscale * pow2f(max(-126, kref - 127 - kUp)), kTiny);
+    // the weight sums' kernel reads the tile as it lies here
+    uint8_t* image = nullptr;
+    if (p.q_image != nullptr && split == 0) {
+      const long long at = ((long long)bk * p.row_tiles + rt) * 2 + tile;
+      image = p.q_image + at * L::TILE;
+      if (row == 0) p.q_scale[at] = qscale;
+    }
+#pragma unroll
+    for (int i = 0; i < QV; ++i) {
+      const int at = row + 128 * i, r = at / QV, c = at % QV;
+      const uint4 u = i < LPR ? uk[i % LPR] : uv[i % LPR];
+      const uint32_t in[4] = {u.x, u.y, u.z, u.w};
+      uint32_t h[4];
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        const float2 f = pair_to_float2(in[x], p.fp16);
+        const __half2 hh = __floats2half2_rn(f.x * down, f.y * down);
+        h[x] = tile * 128 + r < r_cnt ? *reinterpret_cast<const uint32_t*>(&hh) : 0u;
+      }
+      const uint32_t off = (c >> 3) * 16384 + r * 128 + (((c & 7) ^ (r & 7)) << 4);
+      sts128(sb + L::OFF_Q + tile * L::TILE + off, make_uint4(h[0], h[1], h[2], h[3]));
+      if (image != nullptr) *reinterpret_cast<uint4*>(image + off) = make_uint4(h[0], h[1], h[2], h[3]);
+    }
+    fence_proxy_async_smem();
   }
+  __syncthreads();
   volatile int never = 0;
 
   if (warp >= 12) {
@@ -258,38 +301,6 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const AttnParams
   } else if (warp >= 8) {
     regs_dec<kPfConvRegs>();
     // -------------------------------------------------------------- converters
-    constexpr int LPR = D / 16, RPI = 32 / LPR;  // lanes per token, tokens per load of a warp
-    const int cw = warp - 8, c = lane % LPR, rr = lane / LPR;
-    const bool bad_pages = misc[2] != 0;
-    // lane l of a batch: tile l / 2, group of 16 tokens 2 cw + (l & 1) of it
-    int l_page = -1, l_ks = 0, l_vs = 0;
-    auto batch = [&](int j0) {
-      const int j = j0 + (lane >> 1);
-      l_page = -1;
-      if (j < nj) {
-        const int tok = span.token(v0 + j) + 32 * cw + 16 * (lane & 1);
-        if (any_visible(p, tok, 16, p_lo, p_hi)) {
-          const int pg = __ldg(trow + (tok >> p.page_log2));
-          if (pg >= 0 && pg < p.num_pages) {
-            l_page = pg;
-            l_ks = __ldg(p.ks + (long long)pg * p.Hkv + hk);
-            l_vs = __ldg(p.vs + (long long)pg * p.Hkv + hk);
-          }
-        }
-      }
-    };
-    // Unconditional loads (a group that is not to be read takes page 0 and is zeroed below): a
-    // load under a branch would be waited for where the branches join.
-    auto load = [&](const uint8_t* base, int j, uint4 (&u)[LPR]) {
-      const int tok = span.token(v0 + j) + 32 * cw;
-#pragma unroll
-      for (int g = 0; g < 2; ++g) {
-        const int pg = max(0, __shfl_sync(0xffffffffu, l_page, 2 * (j & 15) + g));
-        const uint8_t* at = base + ((((long long)pg * p.Hkv + hk) << p.page_log2) + ((tok + 16 * g) & (page_tok - 1)) + rr) * D + 16 * c;
-#pragma unroll
-        for (int i = 0; i < LPR / 2; ++i) u[g * (LPR / 2) + i] = ldg16_now(at + i * RPI * D);
-      }
-    };
     // the loaded rows as FP16 into a tile; where `edge` says so, rows that no query row sees or
     // whose page is not of the pool become zero (their codes may be NaN)
     auto store = [&](uint32_t dst, uint4 (&u)[LPR], const __half2 (&m)[2], bool edge, int tok, const bool (&held)[2]) {
@@ -328,10 +339,6 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const AttnParams
       }
     };
     bool ok = true;
-    uint4 uk[LPR], uv[LPR];
-    batch(0);
-    load(p.k, 0, uk);
-    load(p.v, 0, uv);
     for (int j = 0; j < nj; ++j) {
       const int st = j & 1, use = j >> 1, tok = span.token(v0 + j);
       const bool edge = bad_pages || !all_visible(p, tok, kPrefillTile, p_lo, p_hi);
@@ -360,7 +367,6 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const AttnParams
       const int pos = r < r_cnt ? s.pos0 + (r_base + r) / p.G : -1;
       const int t_lo = s.pos0 + (r_base + tile * 128) / p.G;
       const int t_hi = s.pos0 + (r_base + min(r_cnt, tile * 128 + 128) - 1) / p.G;
-      const bool bad_pages = misc[2] != 0;
       const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
       const uint32_t s_addr = lane_base + L::S_COL + 128 * tile, o_addr = lane_base + L::O_COL + D * tile;
       const bool idle = tile * 128 + (warp & 3) * 32 >= r_cnt;
@@ -377,7 +383,8 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const AttnParams
           continue;
         }
         uint32_t v[4][32];
-        tmem_ld32(s_addr, v[0]);
+#pragma unroll
+        for (int c4 = 0; c4 < 4; ++c4) tmem_ld32(s_addr + 32 * c4, v[c4]);
         const int tok = span.token(v0 + j);
         const bool edge = bad_pages || !all_visible(p, tok, kPrefillTile, t_lo, t_hi);
         uint32_t see[4] = {0, 0, 0, 0};
@@ -397,12 +404,12 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const AttnParams
             }
           }
         }
-        // the row's maximum, 32 columns at a time while the next are on their way
+        // the row's maximum (all loads are waited for at once: a wait a chunk cost their latency each)
+#pragma unroll
+        for (int c4 = 0; c4 < 4; ++c4) tmem_ld_wait32(v[c4]);
         float mc[4];
 #pragma unroll
         for (int c4 = 0; c4 < 4; ++c4) {
-          tmem_ld_wait32(v[c4]);
-          if (c4 < 3) tmem_ld32(s_addr + 32 * (c4 + 1), v[c4 + 1]);
           if (edge) {
 #pragma unroll
             for (int c = 0; c < 32; ++c)
@@ -473,37 +480,54 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const AttnParams
         if (lane == 0) pf_raise(abort);
       } else {
         tc_fence_after();
-        const long long prow = r < r_cnt ? packed_row(p, s, hk, r_base + r) : 0;
+        const long long prow = r < r_cnt ? packed_row(p, s, hk, r_base + r) : -1;
         // codes' units back to values: 2^(e_ref - 6), in two steps (e_ref may be -127)
         const float back = scale_value((uint32_t)vref), down = 1.0f / (1 << kUp);
         const float f = p.nsplit > 1 ? down : (l > 0.0f ? down / l : 0.0f);
+        // The tile's query rows are done with: each thread leaves its row there (16-byte chunks,
+        // swizzled as the operands are) and the warp writes its 32 rows out in whole lines;
+        // a partial output's FP32 rows go in two halves.
+        const uint32_t stage = sb + L::OFF_Q + tile * L::TILE;
+        const bool part = p.nsplit > 1;
+        for (int half = 0; half < (part ? 2 : 1); ++half) {
 #pragma unroll
-        for (int c4 = 0; c4 < D / 32; ++c4) {
-          uint32_t o[32];
-          tmem_ld32(o_addr + 32 * c4, o);
-          tmem_ld_wait();
+          for (int c4 = 0; c4 < D / 32; ++c4) {
+            if (part && c4 / (D / 64) != half) continue;
+            uint32_t o[32];
+            tmem_ld32(o_addr + 32 * c4, o);
+            tmem_ld_wait32(o);
 #pragma unroll
-          for (int c = 0; c < 32; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * f * back);
-          if (r < r_cnt) {
-            if (p.nsplit > 1) {
-              uint4* dst = reinterpret_cast<uint4*>(p.part_o + (prow * p.nsplit + split) * D + 32 * c4);
+            for (int c = 0; c < 32; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * f * back);
+            if (!part) {
 #pragma unroll
-              for (int c = 0; c < 8; ++c) dst[c] = make_uint4(o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]);
-            } else {
-              uint4* dst = reinterpret_cast<uint4*>(p.o) + prow * (D / 8) + 4 * c4;
+              for (int c = 0; c < 16; ++c)
+                o[c] = float2_to_pair(__uint_as_float(o[2 * c]), __uint_as_float(o[2 * c + 1]), p.fp16);
+            }
+            const int ch0 = part ? 8 * (c4 % (D / 64)) : 4 * c4;
 #pragma unroll
-              for (int c = 0; c < 4; ++c) {
-                uint32_t w[4];
-#pragma unroll
-                for (int x = 0; x < 4; ++x)
-                  w[x] = float2_to_pair(__uint_as_float(o[8 * c + 2 * x]), __uint_as_float(o[8 * c + 2 * x + 1]), p.fp16);
-                dst[c] = make_uint4(w[0], w[1], w[2], w[3]);
-              }
+            for (int c = 0; c < 8; ++c) {
+              if (!part && c >= 4) continue;
+              const int ch = ch0 + c;
+              sts128(stage + (ch >> 3) * 16384 + row * 128 + (((ch & 7) ^ (row & 7)) << 4),
+                     make_uint4(o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]));
             }
           }
+          __syncwarp();
+#pragma unroll 4
+          for (int i = 0; i < QV; ++i) {
+            const int at = lane + 32 * i, rl = at / QV, ch = at % QV, rw = (warp & 3) * 32 + rl;
+            const uint4 x = *reinterpret_cast<const uint4*>(smem + L::OFF_Q + tile * L::TILE + (ch >> 3) * 16384 + rw * 128 +
+                                                            (((ch & 7) ^ (rw & 7)) << 4));
+            const long long to = __shfl_sync(0xffffffffu, prow, rl);
+            if (to >= 0) {
+              if (part) reinterpret_cast<uint4*>(p.part_o)[(to * p.nsplit + split) * (D / 4) + half * QV + ch] = x;
+              else reinterpret_cast<uint4*>(p.o)[to * QV + ch] = x;
+            }
+          }
+          __syncwarp();
         }
         if (r < r_cnt) {
-          if (p.nsplit > 1) p.part_ml[prow * p.nsplit + split] = make_float2(l > 0.0f ? m_ref - kPfShift : -INFINITY, l);
+          if (part) p.part_ml[prow * p.nsplit + split] = make_float2(l > 0.0f ? m_ref - kPfShift : -INFINITY, l);
           else write_lse(p, prow, m_ref - kPfShift, l);
         }
       }
