@@ -20,11 +20,13 @@ struct AppendParams {
 };
 
 // One CTA per (page that a sequence's new tokens touch, kv head, K or V); it owns the page,
-// so the exponent's rise and the codes need no atomics.  A thread holds its rows' 16-bit
-// inputs in registers (at most 8 x 16 bytes) between the maximum and the codes, so the
-// inputs are read once: the append is bound by HBM (2 + 1 bytes an element).  The maximum of
-// |x| is taken on the 15 low bits, which order like the values in both types.
-template <int D>
+// so the exponent's rise and the codes need no atomics.  A thread holds its NV 16-byte vectors
+// in registers between the maximum and the codes, so the inputs are read once: the append is
+// bound by HBM (2 + 1 bytes an element).  The loads have no branch (past the end they take the
+// last vector again, which changes no maximum): under a branch each was waited for by itself
+// (4 x 8192 tokens of 8 heads of 128: 49 us, now APPUS).  The maximum of |x| is taken on the 15 low
+// bits, which order like the values in both types.
+template <int D, int NV>
 __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendParams p) {
   constexpr int VR = D / 8;  // 16-byte vectors per row
   const int b = blockIdx.z, h = blockIdx.y >> 1, op = blockIdx.y & 1;
@@ -42,16 +44,15 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendPara
   const int lo = max(start, col * p.page), hi = min(s.len, (col + 1) * p.page);
   const int items = (hi - lo) * VR;
   const uint4* src = p.x[op] + (long long)(s.q0 + lo - s.pos0) * p.stride[op] + h * VR;
-  uint4 v[8];
+  uint4 v[NV];
   uint32_t am = 0;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int it = threadIdx.x + i * kAppendThreads;
-    v[i] = make_uint4(0, 0, 0, 0);
-    if (it < items) v[i] = __ldg(src + (long long)(it / VR) * p.stride[op] + it % VR);
+  for (int i = 0; i < NV; ++i) {
+    const int it = min((int)threadIdx.x + i * kAppendThreads, items - 1);
+    v[i] = ldg16_now(src + (long long)(it / VR) * p.stride[op] + it % VR);
   }
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
+  for (int i = 0; i < NV; ++i) {
     am = __vmaxu2(am, __vmaxu2(v[i].x & 0x7FFF7FFFu, v[i].y & 0x7FFF7FFFu));
     am = __vmaxu2(am, __vmaxu2(v[i].z & 0x7FFF7FFFu, v[i].w & 0x7FFF7FFFu));
   }
@@ -83,7 +84,7 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendPara
   if (threadIdx.x == 0) *sc = (uint8_t)(e + 127);
   const float m = pow2f(-e);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
+  for (int i = 0; i < NV; ++i) {
     const int it = threadIdx.x + i * kAppendThreads;
     if (it >= items) break;
     const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
@@ -95,6 +96,14 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendPara
     }
     reinterpret_cast<uint2*>(dst + held * D)[it] = make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
   }
+}
+
+template <int D>
+static void launch_append(const AppendParams& p, int vectors, dim3 grid, cudaStream_t s) {
+  if (vectors <= 1) append_kernel<D, 1><<<grid, kAppendThreads, 0, s>>>(p);
+  else if (vectors == 2) append_kernel<D, 2><<<grid, kAppendThreads, 0, s>>>(p);
+  else if (vectors == 4) append_kernel<D, 4><<<grid, kAppendThreads, 0, s>>>(p);
+  else append_kernel<D, 8><<<grid, kAppendThreads, 0, s>>>(p);
 }
 
 // ---------------------------------------------------------------------------
@@ -120,7 +129,11 @@ __device__ __forceinline__ uint32_t order_key(float x) {
 // One CTA per (sequence, kv head).  The free tokens are [lo, hi) (between the sinks and the
 // recent ones); `want` of them stay.  Three passes of 11, 11 and 10 bits of the key narrow
 // the want-th largest key down to one value; tokens above it stay, and of those equal to it
-// the first ones.  Then each warp counts and writes its own contiguous share in order.
+// the first ones.  A warp takes a contiguous share of the tokens, so that it can count and
+// write its kept ones in order; up to 32 KEYS tokens a warp (max_len <= 1024 KEYS) their keys are
+// loaded once and stay in registers (at 64 heads of up to 32768 tokens 43 us when every pass
+// loaded them again, now SELUS).
+template <int KEYS>
 __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const SelectParams p) {
   __shared__ uint32_t hist[2048];
   __shared__ uint32_t wsum[32], wties[32];
@@ -146,89 +159,92 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const SelectP
     return;
   }
   const int lo = p.sinks, hi = n - p.recent;  // keep >= sinks + recent and n > keep: lo < hi
-  uint32_t left = (uint32_t)(m - p.sinks - p.recent), prefix = 0;
-  if (left > 0) {
-    for (int pass = 0; pass < 3; ++pass) {
-      const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0), bits = pass == 2 ? 10 : 11;
-      for (int i = tid; i < 2048; i += kSelThreads) hist[i] = 0;
-      __syncthreads();
-      for (int t = lo + tid; t < hi; t += kSelThreads) {
-        const uint32_t k = order_key(w[t]);
-        if (pass == 0 || (k >> (shift + bits)) == (prefix >> (shift + bits)))
-          atomicAdd(&hist[(k >> shift) & ((1u << bits) - 1u)], 1u);
-      }
-      __syncthreads();
-      // the bin that holds the left-th largest: suffix sums over the bins, 64 a lane
-      if (warp == 0) {
-        const int per = (1 << bits) / 32;
-        uint32_t own = 0;
-        for (int i = 0; i < per; ++i) own += hist[lane * per + ((i + lane) & (per - 1))];
-        uint32_t above = own;  // inclusive suffix sum over lanes
+  const int steps = (n + kSelThreads - 1) / kSelThreads, w0 = warp * steps * 32 + lane;  // this lane's tokens: w0 + 32 i
+  float x[KEYS > 0 ? KEYS : 1];
+  if constexpr (KEYS > 0) {
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const uint32_t y = __shfl_down_sync(0xffffffffu, above, o);
-          if (lane + o < 32) above += y;
-        }
-        above -= own;  // tokens in higher lanes' bins
-        if (above < left && above + own >= left) {
-          for (int i = per - 1; i >= 0; --i) {
-            const uint32_t c = hist[lane * per + i];
-            if (above + c >= left) {
-              s_prefix = prefix | ((uint32_t)(lane * per + i) << shift);
-              s_left = left - above;
-              break;
-            }
-            above += c;
-          }
-        }
+    for (int i = 0; i < KEYS; ++i) x[i] = ldg4_now(w + min(w0 + 32 * min(i, steps - 1), n - 1));
+  }
+  auto each = [&](auto&& f) {  // f(token, weight) for this lane's tokens, in step with the warp
+    if constexpr (KEYS > 0) {
+#pragma unroll
+      for (int i = 0; i < KEYS; ++i) {
+        if (i >= steps) break;
+        f(w0 + 32 * i, x[i]);
       }
-      __syncthreads();
-      prefix = s_prefix;
-      left = s_left;
+    } else {
+#pragma unroll 4
+      for (int i = 0; i < steps; ++i) f(w0 + 32 * i, __ldg(w + min(w0 + 32 * i, n - 1)));
     }
+  };
+  uint32_t left = (uint32_t)(m - p.sinks - p.recent), prefix = 0;
+  const bool any = left > 0;
+  for (int pass = 0; any && pass < 3; ++pass) {
+    const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0), bits = pass == 2 ? 10 : 11;
+    hist[tid] = hist[tid + 1024] = 0;
+    __syncthreads();
+    each([&](int t, float v) {
+      const uint32_t k = order_key(v);
+      if (t >= lo && t < hi && (pass == 0 || (k >> (shift + bits)) == (prefix >> (shift + bits))))
+        atomicAdd(&hist[(k >> shift) & ((1u << bits) - 1u)], 1u);
+    });
+    __syncthreads();
+    // the bin that holds the left-th largest: suffix sums, two bins a thread
+    const uint2 c = reinterpret_cast<const uint2*>(hist)[tid];
+    uint32_t above = c.x + c.y;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t y = __shfl_down_sync(0xffffffffu, above, o);
+      if (lane + o < 32) above += y;
+    }
+    if (lane == 0) wsum[warp] = above;
+    __syncthreads();
+    above += __reduce_add_sync(0xffffffffu, lane > warp ? wsum[lane] : 0u);
+    above -= c.x + c.y;  // tokens in higher bins
+    if (above < left && above + c.x + c.y >= left) {
+      const bool upper = above + c.y >= left;
+      s_prefix = prefix | ((2u * tid + (upper ? 1u : 0u)) << shift);
+      s_left = left - above - (upper ? 0u : c.y);
+    }
+    __syncthreads();
+    prefix = s_prefix;
+    left = s_left;
   }
   // the threshold key is `prefix`, of which the first `left` tokens stay
-  const bool any = m > p.sinks + p.recent;
   auto above = [&](int t, uint32_t k) -> bool { return t < lo || t >= hi || (any && k > prefix); };
-  const int share = ((n + 1023) / 1024) * 32, w0 = warp * share, w1 = min(n, w0 + share);
   uint32_t cnt = 0, ties = 0;
-  for (int t0 = w0; t0 < w1; t0 += 32) {
-    const int t = t0 + lane;
-    const uint32_t k = t < w1 ? order_key(w[t]) : 0u;
-    const bool a = t < w1 && above(t, k);
-    cnt += a;
-    ties += t < w1 && !a && any && k == prefix;
-  }
+  each([&](int t, float v) {
+    const uint32_t k = order_key(v);
+    const bool a = above(t, k);
+    cnt += t < n && a;
+    ties += t < n && !a && any && k == prefix;
+  });
   cnt = __reduce_add_sync(0xffffffffu, cnt);
   ties = __reduce_add_sync(0xffffffffu, ties);
+  __syncthreads();
   if (lane == 0) {
     wsum[warp] = cnt;
     wties[warp] = ties;
   }
   __syncthreads();
-  uint32_t at = 0, tie_at = 0;  // kept tokens and ties before this warp's share
-  for (int i = 0; i < warp; ++i) {
-    at += wsum[i];
-    tie_at += wties[i];
-  }
+  // kept tokens and ties before this warp's share
+  uint32_t at = __reduce_add_sync(0xffffffffu, lane < warp ? wsum[lane] : 0u);
+  uint32_t tie_at = __reduce_add_sync(0xffffffffu, lane < warp ? wties[lane] : 0u);
   at += min(tie_at, left);
-  for (int t0 = w0; t0 < w1; t0 += 32) {
-    const int t = t0 + lane;
-    const float x = t < w1 ? w[t] : 0.0f;
-    const uint32_t k = order_key(x);
-    const bool a = t < w1 && above(t, k), tie = t < w1 && !a && any && k == prefix;
-    const uint32_t below = (1u << lane) - 1u;
+  each([&](int t, float v) {
+    const uint32_t k = order_key(v), below = (1u << lane) - 1u;
+    const bool a = t < n && above(t, k), tie = t < n && !a && any && k == prefix;
     const uint32_t bt = __ballot_sync(0xffffffffu, tie);
     const bool stay = a || (tie && tie_at + __popc(bt & below) < left);
     const uint32_t bs = __ballot_sync(0xffffffffu, stay);
     if (stay) {
       const uint32_t r = at + __popc(bs & below);
       kept[r] = t;
-      dw[r] = x;
+      dw[r] = v;
     }
     at += __popc(bs);
     tie_at += __popc(bt);
-  }
+  });
 }
 
 struct MoveParams {
@@ -281,23 +297,31 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const MovePara
   __syncthreads();
   const long long dh = (long long)dp * p.Hkv + h;
   if (threadIdx.x < 2) p.dsc[threadIdx.x][dh] = (uint8_t)top[threadIdx.x];
+  // four vectors each of K and V a thread and turn, loaded without a branch (a token of no
+  // page takes row 0 and becomes zero)
+  for (int i0 = threadIdx.x; i0 < cnt * VR; i0 += 4 * kMoveThreads) {
+    uint4 w[2][4];
 #pragma unroll
-  for (int o = 0; o < 2; ++o) {
-    uint4* dst = reinterpret_cast<uint4*>(p.dst[o] + dh * p.page * D);
-    const uint4* src = reinterpret_cast<const uint4*>(p.src[o]);
-#pragma unroll 4
-    for (int i = threadIdx.x; i < cnt * VR; i += kMoveThreads) {
-      const int s = i / VR;
-      const long long r = row[s];
-      uint4 w = make_uint4(0, 0, 0, 0);
-      if (r >= 0) w = __ldg(src + r * VR + i % VR);
-      const int k = top[o] - (int)sc[o][s];
-      if (k > 0) {
-        const __half2 down = recode_factor(k);
-        w = make_uint4(recode4(w.x, down), recode4(w.y, down), recode4(w.z, down), recode4(w.w, down));
+    for (int o = 0; o < 2; ++o)
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int i = min(i0 + u * kMoveThreads, cnt * VR - 1);
+        w[o][u] = ldg16_now(p.src[o] + max(row[i / VR], 0ll) * D + 16 * (i % VR));
       }
-      dst[i] = w;
-    }
+#pragma unroll
+    for (int o = 0; o < 2; ++o)
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int i = i0 + u * kMoveThreads;
+        if (i >= cnt * VR) break;
+        const int s = i / VR, k = top[o] - (int)sc[o][s];
+        uint4 x = row[s] >= 0 ? w[o][u] : make_uint4(0, 0, 0, 0);
+        if (k > 0) {
+          const __half2 down = recode_factor(k);
+          x = make_uint4(recode4(x.x, down), recode4(x.y, down), recode4(x.z, down), recode4(x.w, down));
+        }
+        reinterpret_cast<uint4*>(p.dst[o] + dh * p.page * D)[i] = x;
+      }
   }
 }
 
@@ -325,10 +349,10 @@ cudaError_t launch_kv8_append(const Kv8Args& a, const void* k, int64_t k_stride,
   const int pages = (a.s.max_len + a.s.page - 1) / a.s.page;
   const int touched = (a.s.max_q + a.s.page - 2) / a.s.page + 1;
   const dim3 grid(touched < pages ? touched : pages, 2 * a.s.Hkv, a.s.B);
-  if (a.s.d == 128)
-    kv8::append_kernel<128><<<grid, kv8::kAppendThreads, 0, s>>>(p);
-  else
-    kv8::append_kernel<64><<<grid, kv8::kAppendThreads, 0, s>>>(p);
+  // vectors a thread: a page's over the CTA's threads
+  const int vectors = a.s.page * (a.s.d / 8) / kv8::kAppendThreads;
+  if (a.s.d == 128) kv8::launch_append<128>(p, vectors, grid, s);
+  else kv8::launch_append<64>(p, vectors, grid, s);
   count_launches(1);
   return cudaGetLastError();
 }
@@ -338,7 +362,9 @@ cudaError_t launch_kv8_evict(const Kv8Args& a, const Kv8Evict& e, cudaStream_t s
   p.w = e.w; p.lens = a.lens; p.dst_w = e.dst_w; p.dst_lens = e.dst_lens; p.kept = e.kept;
   p.w_cols = e.w_cols; p.dst_w_cols = e.dst_w_cols;
   p.Hkv = a.s.Hkv; p.keep = e.keep; p.sinks = e.sinks; p.recent = e.recent; p.max_len = a.s.max_len;
-  kv8::evict_select_kernel<<<a.s.B * a.s.Hkv, kv8::kSelThreads, 0, s>>>(p);
+  if (a.s.max_len <= 8 * 1024) kv8::evict_select_kernel<8><<<a.s.B * a.s.Hkv, kv8::kSelThreads, 0, s>>>(p);
+  else if (a.s.max_len <= 32 * 1024) kv8::evict_select_kernel<32><<<a.s.B * a.s.Hkv, kv8::kSelThreads, 0, s>>>(p);
+  else kv8::evict_select_kernel<0><<<a.s.B * a.s.Hkv, kv8::kSelThreads, 0, s>>>(p);
   kv8::MoveParams m;
   m.src[0] = a.cache.k; m.src[1] = a.cache.v; m.ssc[0] = a.cache.ks; m.ssc[1] = a.cache.vs;
   m.dst[0] = e.dst.k; m.dst[1] = e.dst.v; m.dsc[0] = e.dst.ks; m.dsc[1] = e.dst.vs;
