@@ -26,8 +26,9 @@ struct AppendParams {
 // last vector again, which changes no maximum): under a branch each was waited for by itself
 // (4 x 8192 tokens of 8 heads of 128: 49 us, now APPUS).  The maximum of |x| is taken on the 15 low
 // bits, which order like the values in both types.
+// Its CTAs are short chains of latencies, so as many as fit are kept on an SM.
 template <int D, int NV>
-__global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendParams p) {
+__global__ void __launch_bounds__(kAppendThreads, NV <= 4 ? 8 : 5) append_kernel(const AppendParams p) {
   constexpr int VR = D / 8;  // 16-byte vectors per row
   const int b = blockIdx.z, h = blockIdx.y >> 1, op = blockIdx.y & 1;
   const Seq s = load_seq(p.lens, p.cu, b, p.n, p.max_q, p.max_len);
@@ -43,13 +44,14 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendPara
   }
   const int lo = max(start, col * p.page), hi = min(s.len, (col + 1) * p.page);
   const int items = (hi - lo) * VR;
-  const uint4* src = p.x[op] + (long long)(s.q0 + lo - s.pos0) * p.stride[op] + h * VR;
+  const long long stride = op ? p.stride[1] : p.stride[0];
+  const uint4* src = (op ? p.x[1] : p.x[0]) + (long long)(s.q0 + lo - s.pos0) * stride + h * VR;
   uint4 v[NV];
   uint32_t am = 0;
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const int it = min((int)threadIdx.x + i * kAppendThreads, items - 1);
-    v[i] = ldg16_now(src + (long long)(it / VR) * p.stride[op] + it % VR);
+    v[i] = ldg16_now(src + (long long)(it / VR) * stride + it % VR);
   }
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
@@ -60,7 +62,7 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendPara
   am = __reduce_max_sync(0xffffffffu, am);
   __shared__ uint32_t wmax[kAppendThreads / 32];
   if ((threadIdx.x & 31) == 0) wmax[threadIdx.x >> 5] = am;
-  uint8_t* sc = p.scales[op] + (long long)page * p.Hkv + h;
+  uint8_t* sc = (op ? p.scales[1] : p.scales[0]) + (long long)page * p.Hkv + h;
   const int e_old = (int)*sc - 127;  // read by every thread before the barrier, written after it
   __syncthreads();
 #pragma unroll
@@ -68,7 +70,7 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendPara
   // the smallest e >= -127 with amax <= 448 * 2^e = 1.75 * 2^(e + 8)
   const uint32_t bits = __float_as_uint(pair_to_float2(am, p.fp16).x);
   int e = max(-127, (int)(bits >> 23) - 135 + ((bits & 0x7FFFFFu) > 0x600000u ? 1 : 0));
-  uint8_t* dst = p.codes[op] + ((long long)page * p.Hkv + h) * p.page * D;
+  uint8_t* dst = (op ? p.codes[1] : p.codes[0]) + ((long long)page * p.Hkv + h) * p.page * D;
   const int held = lo - col * p.page;  // tokens of the sequence already in the page
   if (held > 0) {
     if (e > e_old) {
@@ -263,7 +265,7 @@ constexpr int kMoveThreads = 256;
 // the difference (copied where there is none).  Bound by HBM: every kept row is read and
 // written once, in whole rows of D bytes.
 template <int D>
-__global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const MoveParams p) {
+__global__ void __launch_bounds__(kMoveThreads, 6) evict_move_kernel(const MoveParams p) {
   constexpr int VR = D / 16;
   const int j = blockIdx.x, h = blockIdx.y, b = blockIdx.z;
   __shared__ long long row[128];  // source row, -1: none
@@ -280,6 +282,7 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const MovePara
   }
   if (threadIdx.x < 2) top[threadIdx.x] = 0;
   __syncthreads();
+  int most[2] = {0, 0};
   if ((int)threadIdx.x < cnt) {
     const int t = __ldg(p.kept + ((long long)b * p.Hkv + h) * p.keep + r0 + threadIdx.x);
     const int pg = __ldg(p.table + (long long)b * p.table_cols + t / p.page);
@@ -291,27 +294,33 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const MovePara
     for (int o = 0; o < 2; ++o) {
       const uint8_t c = ok ? __ldg(p.ssc[o] + ph) : 0;
       sc[o][threadIdx.x] = c;
-      atomicMax(&top[o], (int)c);
+      most[o] = c;
     }
+  }
+#pragma unroll
+  for (int o = 0; o < 2; ++o) {
+    const int c = __reduce_max_sync(0xffffffffu, most[o]);
+    if ((threadIdx.x & 31) == 0 && c > 0) atomicMax(&top[o], c);
   }
   __syncthreads();
   const long long dh = (long long)dp * p.Hkv + h;
   if (threadIdx.x < 2) p.dsc[threadIdx.x][dh] = (uint8_t)top[threadIdx.x];
-  // four vectors each of K and V a thread and turn, loaded without a branch (a token of no
+  // UN vectors each of K and V a thread and turn, loaded without a branch (a token of no
   // page takes row 0 and becomes zero)
-  for (int i0 = threadIdx.x; i0 < cnt * VR; i0 += 4 * kMoveThreads) {
-    uint4 w[2][4];
+  constexpr int UN = 2;
+  for (int i0 = threadIdx.x; i0 < cnt * VR; i0 += UN * kMoveThreads) {
+    uint4 w[2][UN];
 #pragma unroll
     for (int o = 0; o < 2; ++o)
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
+      for (int u = 0; u < UN; ++u) {
         const int i = min(i0 + u * kMoveThreads, cnt * VR - 1);
-        w[o][u] = ldg16_now(p.src[o] + max(row[i / VR], 0ll) * D + 16 * (i % VR));
+        w[o][u] = ldg16_now((o ? p.src[1] : p.src[0]) + max(row[i / VR], 0ll) * D + 16 * (i % VR));
       }
 #pragma unroll
     for (int o = 0; o < 2; ++o)
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
+      for (int u = 0; u < UN; ++u) {
         const int i = i0 + u * kMoveThreads;
         if (i >= cnt * VR) break;
         const int s = i / VR, k = top[o] - (int)sc[o][s];
