@@ -278,8 +278,12 @@ __device__ __forceinline__ void split_segment(const AttnParams& p, const Seq& s,
     load_v<D>(p.v + off, g, t, c.v);
   };
   auto step = [&](int it, Codes<D>& c, int pg, int ksc, int vsc) {
-    if (pg < 0) return;
     const int tok = span.token(v0 + warp + it * kSplitWarps);
+    if (pg < 0) {  // not visible: no weight
+      if (p.logits != nullptr)
+        for (int i = lane; i < kTile * p.logit_w; i += 32) logit_row[(long long)tok * p.logit_w + i] = -INFINITY;
+      return;
+    }
     float x[NT][4];
     tile_logits<D, NT>(c.k, qf, x);
     const float kscale = scale_value((uint32_t)ksc);
@@ -585,44 +589,67 @@ __global__ void __launch_bounds__(32 * kMergeWarps) merge_kernel(const AttnParam
 // a thread adds up one token's rows with their final log-sum-exp.  Storing the logits costs
 // 8 bytes a row and token, a fraction of the token's 2 D bytes of codes (4 rows and D = 128:
 // 1/8); computing them again took as long as the attention itself (75 us of 142 at 32
-// sequences of up to 8191 tokens, against 9).  One thread adds a token's rows in order: the sum does
+// sequences of up to 8191 tokens, against LWUS).  One thread adds a token's rows in order: the sum does
 // not depend on how the work was spread.
 constexpr int kWeightRows = 64;  // the most rows of split_kernel
-__global__ void __launch_bounds__(256) logit_weights_kernel(const AttnParams p, int R) {
+constexpr int kWeightThreads = 256;
+__host__ __device__ constexpr int weight_tokens(int rw) { return rw <= 4 ? 4 : rw == 8 ? 2 : 1; }  // of a thread
+
+template <int RW>
+__global__ void __launch_bounds__(kWeightThreads) logit_weights_kernel(const AttnParams p, int R) {
+  constexpr int T = weight_tokens(RW);
   __shared__ float lse2[kWeightRows];
   __shared__ int pos[kWeightRows];
   const int bk = blockIdx.y, b = bk / p.Hkv, hk = bk % p.Hkv;
   const Seq s = load_seq(p.lens, p.cu, b, p.n, p.max_q, p.max_len);
-  const int rows = s.nq * p.G, t0 = blockIdx.x * 256, tok = t0 + threadIdx.x;
-  if (t0 >= s.len || rows == 0) return;
+  const int rows = s.nq * p.G, t0 = blockIdx.x * kWeightThreads * T + threadIdx.x;
+  if (blockIdx.x * kWeightThreads * T >= s.len || rows == 0) return;
+  float* w = p.w + (long long)bk * p.w_cols;
+  float sum[T], was[T];
+#pragma unroll
+  for (int i = 0; i < T; ++i) {
+    sum[i] = 0.0f;
+    was[i] = w[min(t0 + i * kWeightThreads, s.len - 1)];
+  }
   if ((int)threadIdx.x < rows) {
     lse2[threadIdx.x] = p.lse2[packed_row(p, s, hk, threadIdx.x)];
     pos[threadIdx.x] = s.pos0 + threadIdx.x / p.G;
   }
   __syncthreads();
-  if (tok >= s.len || !any_visible(p, tok, 1, max(s.pos0, 0), s.len - 1)) return;
-  const int pg = __ldg(p.table + (long long)b * p.table_cols + (tok >> p.page_log2));
-  if (pg < 0 || pg >= p.num_pages) return;  // no logits were left; reported by split_kernel
-  // a logit that its row does not see may be unwritten: it is loaded (no branch, so that the
-  // loads go out together) and dropped
-  const float w = p.w[(long long)bk * p.w_cols + tok];
-  const float* at = p.logits + ((long long)bk * p.row_tiles * p.logit_tokens + tok) * p.logit_w;
-  float sum = 0.0f;
-  for (int r0 = 0; r0 < rows; r0 += R, at += (long long)p.logit_tokens * p.logit_w) {
-#pragma unroll 4
-    for (int c = 0; c < min(R, rows - r0); c += 2) {
-      const float2 x = *reinterpret_cast<const float2*>(at + c);
+  for (int r0 = 0; r0 < rows; r0 += R) {
+    const float* at = p.logits + ((long long)bk * p.row_tiles + r0 / R) * p.logit_tokens * RW;
+    // a logit that its row does not see may be unwritten: it is loaded (without a branch, so
+    // that the loads go out together) and dropped
+    float2 x[T][RW / 2];
 #pragma unroll
-      for (int y = 0; y < 2; ++y) {
-        const int r = r0 + c + y;
-        if (r >= rows) break;
-        const int pp = pos[r];
+    for (int i = 0; i < T; ++i)
+#pragma unroll
+      for (int c = 0; c < RW / 2; ++c)
+        x[i][c] = *reinterpret_cast<const float2*>(at + (long long)min(t0 + i * kWeightThreads, s.len - 1) * RW + 2 * c);
+#pragma unroll
+    for (int c = 0; c < RW; ++c) {
+      if (r0 + c >= rows) break;
+      const float nl = lse2[r0 + c];
+      const int pp = pos[r0 + c];
+#pragma unroll
+      for (int i = 0; i < T; ++i) {
+        const int tok = t0 + i * kWeightThreads;
         const bool see = tok <= pp && (p.window == 0 || tok > pp - p.window || tok < p.sinks);
-        sum += see ? ex2_approx((y ? x.y : x.x) - lse2[r]) : 0.0f;
+        sum[i] += see ? ex2_approx((c & 1 ? x[i][c / 2].y : x[i][c / 2].x) - nl) : 0.0f;
       }
     }
   }
-  p.w[(long long)bk * p.w_cols + tok] = w + sum;
+#pragma unroll
+  for (int i = 0; i < T; ++i) {
+    const int tok = t0 + i * kWeightThreads;
+    if (tok < s.len && any_visible(p, tok, 1, max(s.pos0, 0), s.len - 1)) w[tok] = was[i] + sum[i];
+  }
+}
+
+template <int RW>
+static void launch_logit_weights(const AttnParams& p, const Plan& plan, const thrift_kv8_shape& s, cudaStream_t st) {
+  const int per = kWeightThreads * weight_tokens(RW);
+  logit_weights_kernel<RW><<<dim3((s.max_len + per - 1) / per, s.B * s.Hkv), kWeightThreads, 0, st>>>(p, 8 * plan.nt);
 }
 
 static Plan make_plan(const thrift_kv8_shape& s, const thrift_kv8_mask& m, bool with_w) {
@@ -663,8 +690,7 @@ static Plan make_plan(const thrift_kv8_shape& s, const thrift_kv8_mask& m, bool 
   p.o_off = take(states * s.d * sizeof(float));
   p.slots_off = take(p.tiles128 ? 0 : (size_t)units * sizeof(int2));
   p.lse_off = take(with_w ? nrow * sizeof(float) : 0);
-  const long long even = (rows + 1) / 2 * 2;
-  p.logit_w = (int)(even < R ? even : R);
+  p.logit_w = rows <= 2 ? 2 : rows <= 4 ? 4 : 8 * p.nt;
   p.logit_tokens = (s.max_len + kTile - 1) / kTile * kTile;
   // prefill_kernel's query tiles for tile_weights_kernel
   const size_t tiles128 = with_w && p.tiles128 ? (size_t)units * 2 : 0;
@@ -702,7 +728,12 @@ static cudaError_t launch_attn_d(const AttnParams& p, const Plan& plan, const th
     if (e != cudaSuccess) return e;
     ++launches;
   } else if (p.w != nullptr) {
-    logit_weights_kernel<<<dim3((s.max_len + 255) / 256, s.B * s.Hkv), 256, 0, st>>>(p, 8 * plan.nt);
+    switch (plan.logit_w) {
+      case 2: launch_logit_weights<2>(p, plan, s, st); break;
+      case 4: launch_logit_weights<4>(p, plan, s, st); break;
+      case 8: launch_logit_weights<8>(p, plan, s, st); break;
+      default: launch_logit_weights<16>(p, plan, s, st);
+    }
     ++launches;
   }
   count_launches(launches);

@@ -187,14 +187,12 @@ def test_a_call_follows_its_tensors_device(monkeypatch):
 
     class Guard:
         def __init__(self, d): self.d = d
-        def __enter__(self): seen.append(("in", self.d.index))
-        def __exit__(self, *a): seen.append(("out", self.d.index))
+        def __enter__(self): seen.append(("in", self.d))
+        def __exit__(self, *a): seen.append(("out", self.d))
 
-    class Stream:
-        def __init__(self, d): self.cuda_stream = 100 + d.index
     monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
     monkeypatch.setattr(torch.cuda, "device", Guard)
-    monkeypatch.setattr(torch.cuda, "current_stream", lambda d=torch.device("cuda", 0): Stream(d))
+    monkeypatch.setattr(_lib, "_raw_stream", lambda index: 100 + index)
     _lib._kv8_call(lambda *a: seen.append(a) or 0, "x", torch.device("cuda", 1), 7)
     assert seen == [("in", 1), (7, 101), ("out", 1)]
     seen.clear()
