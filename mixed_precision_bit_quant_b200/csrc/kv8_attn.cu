@@ -9,6 +9,7 @@
 //   split_kernel   few rows: every CTA takes the same share of all visible tokens of all tiles
 //                  of 8 or 16 rows; online softmax; writes the output, or a run's
 //                  state (maximum, sum, unnormalised output) where several CTAs share a tile
+//   cluster_kernel few rows of short units: a cluster takes one and joins its states itself
 //   prefill_kernel (kv8_prefill.cu) many rows
 //   merge_kernel   joins the runs' states of a row
 //   logit_weights_kernel, tile_weights_kernel (kv8_prefill.cu)  add the rows' final weights to
@@ -211,6 +212,13 @@ __device__ __forceinline__ Share find_share(const AttnParams& p, int B) {
 // e_ref the largest seen, so the products see bare codes; S's fragment becomes P's by one
 // 8x8 transpose.  A row's maximum is raised (and O rescaled) only when a logit
 // exceeds it by 4 binades: the common step needs one vote and no cross-lane maximum.
+// Where a segment's state goes, besides a slot of the workspace.
+constexpr long long kWhole = -1, kToCluster = -2;
+// Shared memory in floats: the warps' outputs, their maxima and sums, then (for a cluster) the
+// CTA's own.
+__host__ __device__ constexpr int cluster_ml_at(int d, int nt) { return kSplitWarps * 8 * nt * (d + 4 + 2); }
+__host__ __device__ constexpr int split_smem(int d, int nt) { return 4 * (cluster_ml_at(d, nt) + 8 * nt * 2); }
+
 template <int D, int NT>
 __device__ __forceinline__ void split_segment(const AttnParams& p, const Seq& s, int b, int hk, int rt, const Span<kTile>& span,
                                               int v0, int v1, long long slot, float* sm) {
@@ -442,7 +450,10 @@ __device__ __forceinline__ void split_segment(const AttnParams& p, const Seq& s,
       o.z += x.z * f;
       o.w += x.w * f;
     }
-    if (slot < 0) {  // the whole unit: final
+    if (slot == kToCluster) {  // left in shared memory for the cluster's other CTAs
+      *reinterpret_cast<float4*>(so + r * (D + 4) + 4 * c4) = o;  // where only this thread has read
+      if (c4 == 0) *reinterpret_cast<float2*>(sm + cluster_ml_at(D, NT) + 2 * r) = make_float2(mm, ll);
+    } else if (slot == kWhole) {  // the whole unit: final
       const long long row = packed_row(p, s, hk, r_base + r);
       const float inv = ll > 0.0f ? 1.0f / ll : 0.0f;
       reinterpret_cast<uint2*>(p.o)[row * (D / 4) + c4] =
@@ -480,7 +491,7 @@ __global__ void __launch_bounds__(kSplitThreads, resident_ctas(D, NT)) split_ker
       const bool whole = v == 0 && v1 == span.count;
       if (v == 0 && threadIdx.x == 0)  // the unit's first slot and how many it has
         p.unit_slots[unit] = make_int2((int)blockIdx.x + unit, (at + span.count - 1) / sh.share - (int)blockIdx.x + 1);
-      split_segment<D, NT>(p, s, b, hk, rt, span, v, v1, whole ? -1 : (long long)blockIdx.x + unit, sm);
+      split_segment<D, NT>(p, s, b, hk, rt, span, v, v1, whole ? kWhole : (long long)blockIdx.x + unit, sm);
       at += v1 - v;
       __syncthreads();  // shared memory is free again
     }
@@ -492,6 +503,70 @@ __global__ void __launch_bounds__(kSplitThreads, resident_ctas(D, NT)) split_ker
       b_c *= p.Hkv;
     }
   }
+}
+
+// A short unit (few tiles, and few units): one cluster of eight CTAs takes it, an eighth of its
+// tiles each, and joins the states through the cluster's shared memory -- no search for the
+// shares, no workspace, no second launch.  At one sequence of 517 tokens and 12 heads of 64
+// CLUS1; at four windows of 4096 tokens CLUS2 (split_kernel and merge_kernel first).
+constexpr int kCluster = 8;
+__device__ __forceinline__ uint32_t peer_address(uint32_t addr, uint32_t rank) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+template <int D, int NT>
+__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kSplitThreads, resident_ctas(D, NT))
+    cluster_kernel(const AttnParams p) {
+  constexpr int R = 8 * NT;
+  extern __shared__ __align__(16) float sm[];
+  const int rank = blockIdx.x % kCluster, unit = blockIdx.x / kCluster;
+  const int rt = unit % p.row_tiles, bk = unit / p.row_tiles, b = bk / p.Hkv, hk = bk % p.Hkv;
+  const Seq s = load_seq(p.lens, p.cu, b, p.n, p.max_q, p.max_len);
+  if (s.bad && threadIdx.x == 0 && rank == 0 && hk == 0 && rt == 0) raise_bad();
+  const int r_base = rt * R, r_cnt = min(s.nq * p.G - r_base, R);
+  if (r_cnt <= 0) return;  // the whole cluster
+  const Span<kTile> span = row_tile_span<R>(p, s, rt);
+  const int v0 = span.count * rank / kCluster, v1 = span.count * (rank + 1) / kCluster;
+  split_segment<D, NT>(p, s, b, hk, rt, span, v0, v1, kToCluster, sm);
+  cluster_sync();
+  const uint32_t so = smem_u32(sm), sml = smem_u32(sm + cluster_ml_at(D, NT));
+  for (int i = rank * kSplitThreads + threadIdx.x; i < r_cnt * (D / 4); i += kCluster * kSplitThreads) {
+    const int r = i / (D / 4), c4 = i % (D / 4);
+    float4 x[kCluster];
+    float2 ml[kCluster];
+    float mm = -INFINITY, ll = 0.0f;
+#pragma unroll
+    for (int k = 0; k < kCluster; ++k) {
+      asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];"
+                   : "=f"(ml[k].x), "=f"(ml[k].y) : "r"(peer_address(sml + 8 * r, k)));
+      asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                   : "=f"(x[k].x), "=f"(x[k].y), "=f"(x[k].z), "=f"(x[k].w)
+                   : "r"(peer_address(so + 4 * (r * (D + 4) + 4 * c4), k)));
+    }
+#pragma unroll
+    for (int k = 0; k < kCluster; ++k) mm = fmaxf(mm, ml[k].x);
+    float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+    for (int k = 0; k < kCluster; ++k) {
+      const float f = ml[k].x == -INFINITY ? 0.0f : ex2_approx(ml[k].x - mm);
+      ll += ml[k].y * f;
+      o.x += x[k].x * f;
+      o.y += x[k].y * f;
+      o.z += x[k].z * f;
+      o.w += x[k].w * f;
+    }
+    const long long row = packed_row(p, s, hk, r_base + r);
+    const float inv = ll > 0.0f ? 1.0f / ll : 0.0f;
+    reinterpret_cast<uint2*>(p.o)[row * (D / 4) + c4] =
+        make_uint2(float2_to_pair(o.x * inv, o.y * inv, p.fp16), float2_to_pair(o.z * inv, o.w * inv, p.fp16));
+    if (c4 == 0) write_lse(p, row, mm, ll);
+  }
+  cluster_sync();  // no CTA leaves while another reads its shared memory
 }
 
 // Joins the runs' states of a row: one CTA per (new token and query head, sequence).  The
@@ -652,8 +727,9 @@ static void launch_logit_weights(const AttnParams& p, const Plan& plan, const th
   logit_weights_kernel<RW><<<dim3((s.max_len + per - 1) / per, s.B * s.Hkv), kWeightThreads, 0, st>>>(p, 8 * plan.nt);
 }
 
+constexpr int kClusterTiles = 12;
 static Plan make_plan(const thrift_kv8_shape& s, const thrift_kv8_mask& m, bool with_w) {
-  Plan p;
+  Plan p{};
   const long long G = s.Hq / s.Hkv, rows = (long long)s.max_q * G;
   p.tiles128 = rows > 64;
   p.nt = rows <= 8 ? 1 : 2;
@@ -673,6 +749,8 @@ static Plan make_plan(const thrift_kv8_shape& s, const thrift_kv8_mask& m, bool 
     if (p.chunk < 2) p.chunk = 2;
   } else {
     const int resident = resident_ctas(s.d, p.nt);
+    // one wave of clusters, and at most kClusterTiles tiles a warp: beyond that a unit needs more CTAs
+    p.cluster = units * kCluster <= 148 * resident && tiles <= kClusterTiles * kCluster * kSplitWarps;
     const long long most = (tiles * units + kSplitWarps - 1) / kSplitWarps;
     p.ctas = (int)(most < 148 * resident ? most : 148 * resident);
   }
@@ -683,12 +761,12 @@ static Plan make_plan(const thrift_kv8_shape& s, const thrift_kv8_mask& m, bool 
     states = p.nsplit > 1 ? nrow * p.nsplit : 0;
   } else {
     p.nsplit = 0;
-    states = (size_t)(p.ctas + units) * R;
+    states = p.cluster ? 0 : (size_t)(p.ctas + units) * R;
   }
   auto take = [&](size_t n) { const size_t o = at; at += (n + 255) / 256 * 256; return o; };
   p.ml_off = take(states * sizeof(float2));
   p.o_off = take(states * s.d * sizeof(float));
-  p.slots_off = take(p.tiles128 ? 0 : (size_t)units * sizeof(int2));
+  p.slots_off = take(p.tiles128 || p.cluster ? 0 : (size_t)units * sizeof(int2));
   p.lse_off = take(with_w ? nrow * sizeof(float) : 0);
   p.logit_w = rows <= 2 ? 2 : rows <= 4 ? 4 : 8 * p.nt;
   p.logit_tokens = (s.max_len + kTile - 1) / kTile * kTile;
@@ -703,7 +781,12 @@ static Plan make_plan(const thrift_kv8_shape& s, const thrift_kv8_mask& m, bool 
 
 template <int D, int NT>
 static void launch_split(const AttnParams& p, const Plan& plan, const thrift_kv8_shape& s, cudaStream_t st) {
-  constexpr int sm = (int)sizeof(float) * kSplitWarps * 8 * NT * (D + 4 + 2);
+  constexpr int sm = split_smem(D, NT);
+  if (plan.cluster) {
+    const unsigned units = (unsigned)(s.B * s.Hkv * plan.row_tiles);
+    cluster_kernel<D, NT><<<units * kCluster, kSplitThreads, sm, st>>>(p);
+    return;
+  }
   split_kernel<D, NT><<<plan.ctas, kSplitThreads, sm, st>>>(p, s.B);
   merge_kernel<D, 8 * NT><<<dim3(s.max_q * s.Hq, s.B), 32 * kMergeWarps, 0, st>>>(p);
 }
@@ -721,7 +804,7 @@ static cudaError_t launch_attn_d(const AttnParams& p, const Plan& plan, const th
   } else {
     if (plan.nt == 1) launch_split<D, 1>(p, plan, s, st);
     else launch_split<D, 2>(p, plan, s, st);
-    ++launches;
+    if (!plan.cluster) ++launches;
   }
   if (p.w != nullptr && plan.tiles128) {
     const cudaError_t e = launch_tile_weights(p, s, st);

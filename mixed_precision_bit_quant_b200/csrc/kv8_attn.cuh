@@ -81,6 +81,7 @@ __device__ __forceinline__ bool all_visible(const AttnParams& p, int a, int n, i
 // How a call is cut up.  The same for the workspace's size and the launch.
 struct Plan {
   bool tiles128;  // prefill_kernel (128-row tiles) instead of split_kernel
+  bool cluster;   // cluster_kernel instead of split_kernel and merge_kernel
   int nt, row_tiles, nsplit, chunk, ctas;
   size_t ml_off, o_off, slots_off, lse_off, logits_off, image_off, scale_off, bytes;
   int logit_w, logit_tokens;

@@ -129,6 +129,11 @@ def _attend(Hq, Hkv, d, page, lens, news, dtype="bf16", window=0, sinks=0, weigh
     (12, 12, 64, 64, [197, 197], [197, 197]),       # the vit sizes, causal
     (4, 2, 128, 64, [1000, 2049], [150, 70]),
     (32, 8, 128, 64, [4097], [1]),                  # many runs
+    # sequences too long for a cluster: shares of all tiles, units cut at any place
+    (6, 2, 64, 32, [7001, 0, 513], [1, 1, 1]),
+    (16, 1, 128, 128, [6400], [1]),
+    (7, 1, 128, 64, [6300, 40, 16], [2, 5, 0]),
+    (20, 2, 64, 16, [6401, 900], [3, 4]),
 ])
 @pytest.mark.parametrize("dtype", ["bf16", "fp16"])
 def test_attention(Hq, Hkv, d, page, lens, news, dtype):
@@ -137,14 +142,15 @@ def test_attention(Hq, Hkv, d, page, lens, news, dtype):
 
 @pytest.mark.parametrize("window,sinks", [(1, 0), (1, 1), (5, 3), (16, 16), (33, 4), (64, 0), (100, 17), (300, 64),
                                           (10 ** 6, 3), (2 ** 31 - 1, 2 ** 31 - 1), (40, 10 ** 6)])
-@pytest.mark.parametrize("lens,news", [([1, 40, 517], [1, 1, 1]), ([300, 129], [140, 33]), ([64, 20], [64, 27])])
+@pytest.mark.parametrize("lens,news", [([1, 40, 517], [1, 1, 1]), ([13001, 700], [1, 1]), ([300, 129], [140, 33]), ([64, 20], [64, 27])])
 def test_window_and_sinks(window, sinks, lens, news):
     _attend(8, 4, 64, 16, lens, news, window=window, sinks=sinks, weights=True, seed=window % 97 + sinks % 89)
 
 
 @pytest.mark.parametrize("Hq,Hkv,d,page,lens,news", [
     (4, 4, 64, 16, [1, 0, 77], [1, 1, 1]), (8, 1, 128, 64, [1500, 3], [1, 1]), (12, 2, 128, 32, [200, 150], [20, 3]),
-    (16, 1, 64, 128, [400], [130]), (6, 6, 128, 16, [513, 511], [512, 511])])
+    (16, 1, 64, 128, [400], [130]), (6, 6, 128, 16, [513, 511], [512, 511]),
+    (6, 2, 64, 32, [7001, 513], [1, 1]), (14, 2, 128, 64, [6300, 40], [2, 5])])
 def test_weight_sums(Hq, Hkv, d, page, lens, news):
     _attend(Hq, Hkv, d, page, lens, news, weights=True, seed=d + page)
 
@@ -260,7 +266,7 @@ def test_bad_lengths_ranges_and_pages_are_reported():
 def test_a_workspace_that_is_too_small_is_refused():
     cache = _pool(40, 2, 64, 128, 0)
     q = torch.zeros((1, 4, 128), dtype=torch.bfloat16, device="cuda")
-    table, lens = _i32(np.arange(32)[None]), _i32([2000])
+    table, lens = _i32(np.arange(32)[None].repeat(8, 1)), _i32([2000])  # max_len 16384: more than a cluster takes
     need = mq.kv8_attention_workspace(q, cache, table, lens)
     assert need > 0
     with pytest.raises(ValueError, match="ws"):
@@ -503,8 +509,8 @@ def test_captured_calls_read_lengths_when_they_run():
 def test_calls_on_two_streams_at_once():
     """Two streams, each with its own workspace, against the same calls one after the other."""
     page, Hkv, Hq, d = 64, 8, 32, 128
-    lens = [5000, 3001]
-    table, P = _tables(lens, page, 80, 1)
+    lens = [9000, 7001]
+    table, P = _tables(lens, page, 150, 1)
     cache = _pool(P, Hkv, page, d, 1, nan=False)
     qs = [torch.randn((2, Hq, d), generator=torch.Generator().manual_seed(i)).to(torch.bfloat16).cuda() for i in (1, 2)]
     t, ln = _i32(table), _i32(lens)
