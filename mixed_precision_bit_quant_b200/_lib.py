@@ -645,15 +645,20 @@ def kv8_evict(cache: Kv8Cache, table: torch.Tensor, lens: torch.Tensor, weights:
     if a < b + 4 * dst_weights.numel() and b < a + 4 * weights.numel():
         raise ValueError("dst_weights: must not overlap weights")
     keep, sinks, recent = int(keep), int(sinks), int(recent)
-    if not all(-2 ** 31 <= x < 2 ** 31 for x in (keep, sinks, recent)):
+    if not (-2 ** 31 <= keep < 2 ** 31 and -2 ** 31 <= sinks < 2 ** 31 and -2 ** 31 <= recent < 2 ** 31):
         raise ValueError("keep, sinks, recent: must fit 32 bits")
     if dst_lens is None:
-        dst_lens = torch.empty((B,), dtype=torch.int32, device=dev)
+        dst_lens = torch.empty_like(lens)
+        lens_ptr = dst_lens.data_ptr()
+    else:
+        lens_ptr = _kv8_ints(dst_lens, "dst_lens", (B,), dev)
     if kept is None:
         kept = torch.empty((B, Hkv, max(keep, 0)), dtype=torch.int32, device=dev)
+        kept_ptr = kept.data_ptr()
+    else:
+        kept_ptr = _kv8_ints(kept, "kept", (B, Hkv, keep), dev)
     _kv8_call(lib().thrift_kv8_evict, "thrift_kv8_evict", dev, shape, cache._ref, tp, lp, a, w_cols, keep, sinks,
-              recent, dst._ref, dtp, dst_table.shape[1],
-              _kv8_ints(dst_lens, "dst_lens", (B,), dev), b, dw_cols, _kv8_ints(kept, "kept", (B, Hkv, keep), dev))
+              recent, dst._ref, dtp, dst_table.shape[1], lens_ptr, b, dw_cols, kept_ptr)
     return dst_lens, kept
 
 

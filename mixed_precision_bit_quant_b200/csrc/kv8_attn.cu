@@ -45,21 +45,27 @@ __device__ __forceinline__ uint32_t movmatrix(uint32_t x) {
 // is exact unless it is 2^31 (BF16) or 2^28 (FP16) times smaller, and then at most 2^-39 of
 // the largest is lost.  Step s pairs k = 2t, 2t+1 and 2t+8, 2t+9 with four
 // consecutive channels, 64 (s / 4) + 16 t + 4 (s % 4) and up, so that a lane's codes of a token
-// are whole 16-byte vectors.  The row's four lanes (t = 0..3) share e; returns it.
+// are whole 16-byte vectors.  The row's four lanes (t = 0..3) share e; scale_query returns it.
 template <int D>
-__device__ __forceinline__ int load_query(const uint32_t* q, int t, bool fp16, uint32_t (&f)[D / 16][2]) {
-  uint32_t am = 0;
+__device__ __forceinline__ void load_query(const uint32_t* q, int t, uint32_t (&f)[D / 16][2]) {
 #pragma unroll
   for (int v = 0; v < D / 64; ++v)
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
-      uint4 u = make_uint4(0, 0, 0, 0);
-      if (q != nullptr) u = __ldg(reinterpret_cast<const uint4*>(q + 32 * v + 8 * t + 4 * x));
+      const uint4 u = ldg16_now(q + 32 * v + 8 * t + 4 * x);
       f[4 * v + 2 * x][0] = u.x;
       f[4 * v + 2 * x][1] = u.y;
       f[4 * v + 2 * x + 1][0] = u.z;
       f[4 * v + 2 * x + 1][1] = u.w;
     }
+}
+template <int D>
+__device__ __forceinline__ int scale_query(bool held, bool fp16, uint32_t (&f)[D / 16][2]) {
+  uint32_t am = 0;
+#pragma unroll
+  for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+    for (int x = 0; x < 2; ++x) f[i][x] = held ? f[i][x] : 0u;
 #pragma unroll
   for (int i = 0; i < D / 16; ++i) am = __vmaxu2(am, __vmaxu2(f[i][0] & 0x7FFF7FFFu, f[i][1] & 0x7FFF7FFFu));
   am = max(am & 0xFFFFu, am >> 16);
@@ -230,24 +236,10 @@ __device__ __forceinline__ void split_segment(const AttnParams& p, const Seq& s,
   float* so = sm;                              // [warps][R][D + 4]
   float* sml = sm + kSplitWarps * R * (D + 4);  // [warps][R][2]
 
+  // the query rows and the first tile's codes are on their way together
   uint32_t qf[NT][D / 16][2];
-  float fs[NT][2];   // per column 2t, 2t+1: logits' scale without the page's
-  int pos[NT][2];    // per column: the query's position
-  float m[NT][2], l[NT][2];
 #pragma unroll
-  for (int n = 0; n < NT; ++n) {
-    const int r = 8 * n + g;
-    const int e = load_query<D>(r < r_cnt ? query_row(p, s, hk, r_base + r, D) : nullptr, t, p.fp16, qf[n]);
-#pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      const int ec = __shfl_sync(0xffffffffu, e, 4 * (2 * t + x));
-      fs[n][x] = pow2f(ec) * p.scale_log2;
-      const int c = 8 * n + 2 * t + x;
-      pos[n][x] = c < r_cnt ? s.pos0 + (r_base + c) / p.G : -1;
-      m[n][x] = -INFINITY;
-      l[n][x] = 0.0f;
-    }
-  }
+  for (int n = 0; n < NT; ++n) load_query<D>(query_row(p, s, hk, r_base + min(8 * n + g, r_cnt - 1), D), t, qf[n]);
   float acc[NT][D / 16][4];
 #pragma unroll
   for (int n = 0; n < NT; ++n)
@@ -285,6 +277,28 @@ __device__ __forceinline__ void split_segment(const AttnParams& p, const Seq& s,
     load_k<D>(p.k + off, g, t, c.k);
     load_v<D>(p.v + off, g, t, c.v);
   };
+  Codes<D> ca, cb;
+  int pa = -1, pbg = -1;
+  if (count > 0) {
+    batch(0);
+    fetch(0, ca, pa);
+  }
+  float fs[NT][2];   // per column 2t, 2t+1: logits' scale without the page's
+  int pos[NT][2];    // per column: the query's position
+  float m[NT][2], l[NT][2];
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+    const int e = scale_query<D>(8 * n + g < r_cnt, p.fp16, qf[n]);
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      const int ec = __shfl_sync(0xffffffffu, e, 4 * (2 * t + x));
+      fs[n][x] = pow2f(ec) * p.scale_log2;
+      const int c = 8 * n + 2 * t + x;
+      pos[n][x] = c < r_cnt ? s.pos0 + (r_base + c) / p.G : -1;
+      m[n][x] = -INFINITY;
+      l[n][x] = 0.0f;
+    }
+  }
   auto step = [&](int it, Codes<D>& c, int pg, int ksc, int vsc) {
     const int tok = span.token(v0 + warp + it * kSplitWarps);
     if (pg < 0) {  // not visible: no weight
@@ -390,12 +404,6 @@ __device__ __forceinline__ void split_segment(const AttnParams& p, const Seq& s,
     }
   };
 
-  Codes<D> ca, cb;
-  int pa = -1, pbg = -1;
-  if (count > 0) {
-    batch(0);
-    fetch(0, ca, pa);
-  }
   for (int it = 0; it < count; it += 2) {
     // the lane that holds a tile's page also holds its scales; a batch is 32 tiles (even)
     int ksc = __shfl_sync(0xffffffffu, l_ks, it & 31), vsc = __shfl_sync(0xffffffffu, l_vs, it & 31);

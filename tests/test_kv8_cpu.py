@@ -82,7 +82,8 @@ def test_bad_heads_and_rows_of_attention():
                                 dict(cache=_cache(0)), dict(cache=_cache(k=None)), dict(cache=_cache(v=24)),
                                 dict(cache=_cache(ks=None)), dict(cache=_cache((1 << 30) + 1))])
 def test_bad_attention_arguments(kw):
-    assert _attn(_shape(max_len=256, table_cols=64, n=2) if "w" not in kw else None, **kw) == INVALID
+    # (long enough that the call needs a workspace)
+    assert _attn(_shape(max_len=65536, table_cols=1024) if "w" not in kw else None, **kw) == INVALID
 
 
 @pytest.mark.parametrize("kw", [dict(k=None), dict(k=24), dict(v=8), dict(ks=248), dict(ks=260), dict(vs=100),
