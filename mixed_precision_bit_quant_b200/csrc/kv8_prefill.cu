@@ -19,7 +19,7 @@ namespace thrift {
 namespace kv8 {
 
 constexpr int kPfThreads = 512;
-constexpr int kPfSoftmaxRegs = 176, kPfConvRegs = 112, kPfOtherRegs = 48;
+constexpr int kPfSoftmaxRegs = 192, kPfConvRegs = 72, kPfOtherRegs = 56;
 static_assert(2 * kPfSoftmaxRegs + kPfConvRegs + kPfOtherRegs <= 512, "register split exceeds the launch budget");
 constexpr uint64_t kPfWaitNs = 2000000000ull;  // 2 s per wait: far above any legitimate wait
 constexpr int kUp = 6;          // codes enter FP16 times 2^6: at most 448 * 64 < 65504
@@ -135,17 +135,13 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const AttnParams
       }
     }
   };
-  // Unconditional loads (a group that is not to be read takes page 0 and is zeroed below): a
-  // load under a branch would be waited for where the branches join.
-  auto load = [&](const uint8_t* base, int j, uint4 (&u)[LPR]) {
-    const int tok = span.token(v0 + j) + 32 * cw;
-#pragma unroll
-    for (int g = 0; g < 2; ++g) {
-      const int pg = max(0, __shfl_sync(0xffffffffu, l_page, 2 * (j & 15) + g));
-      const uint8_t* at = base + ((((long long)pg * p.Hkv + hk) << p.page_log2) + ((tok + 16 * g) & (page_tok - 1)) + rr) * D + 16 * c;
-#pragma unroll
-      for (int i = 0; i < LPR / 2; ++i) u[g * (LPR / 2) + i] = ldg16_now(at + i * RPI * D);
-    }
+  // Where this lane's rows of group g (16 of the warp's 32 tokens) of tile j are.  A group that is not
+  // to be read takes page 0 and is zeroed below: a load under a branch would be waited for
+  // where the branches join.
+  auto place = [&](const uint8_t* base, int j, int g) -> const uint8_t* {
+    const int tok = span.token(v0 + j) + 32 * cw + 16 * g;
+    const int pg = max(0, __shfl_sync(0xffffffffu, l_page, 2 * (j & 15) + g));
+    return base + ((((long long)pg * p.Hkv + hk) << p.page_log2) + (tok & (page_tok - 1)) + rr) * D + 16 * c;
   };
   // The latencies of the start run side by side: the softmax warps load the query rows (whole
   // rows at a time: one row a thread took 4096 wavefronts), the converters the first tile's
@@ -174,8 +170,12 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const AttnParams
     }
   } else if (warp < 12) {
     batch(0);
-    load(p.k, 0, uk);
-    load(p.v, 0, uv);
+#pragma unroll
+    for (int g = 0; g < 2; ++g) {
+      const uint8_t* at = place(p.k, 0, g);
+#pragma unroll
+      for (int i = 0; i < LPR / 2; ++i) uk[g * (LPR / 2) + i] = ldg16_now(at + i * RPI * D);
+    }
   } else {
     int ek = 0, ev = 0;
     bool bad = false;
@@ -301,62 +301,63 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const AttnParams
   } else if (warp >= 8) {
     regs_dec<kPfConvRegs>();
     // -------------------------------------------------------------- converters
-    // the loaded rows as FP16 into a tile; where `edge` says so, rows that no query row sees or
-    // whose page is not of the pool become zero (their codes may be NaN)
-    auto store = [&](uint32_t dst, uint4 (&u)[LPR], const __half2 (&m)[2], bool edge, int tok, const bool (&held)[2]) {
-      if (edge) {
-#pragma unroll
-        for (int g = 0; g < 2; ++g) {
-#pragma unroll
-          for (int i = 0; i < LPR / 2; ++i)
-            if (!held[g] || !any_visible(p, tok + 32 * cw + 16 * g + i * RPI + rr, 1, p_lo, p_hi))
-              u[g * (LPR / 2) + i] = make_uint4(0, 0, 0, 0);
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < LPR; ++i) {
-        const int r = 32 * cw + i * RPI + rr;
-        const __half2 f = m[i * RPI / 16];
-        const uint4 lo = make_uint4(hmul2_u32(e4m3x2_to_h2(u[i].x & 0xFFFFu), f), hmul2_u32(e4m3x2_to_h2(u[i].x >> 16), f),
-                                    hmul2_u32(e4m3x2_to_h2(u[i].y & 0xFFFFu), f), hmul2_u32(e4m3x2_to_h2(u[i].y >> 16), f));
-        const uint4 hi = make_uint4(hmul2_u32(e4m3x2_to_h2(u[i].z & 0xFFFFu), f), hmul2_u32(e4m3x2_to_h2(u[i].z >> 16), f),
-                                    hmul2_u32(e4m3x2_to_h2(u[i].w & 0xFFFFu), f), hmul2_u32(e4m3x2_to_h2(u[i].w >> 16), f));
-        // chunks 2c and 2c + 1 of the row; the row's second half writes them in the other
-        // order, so that eight lanes' stores meet all banks
-        const int ch = 2 * c, blk = ch >> 3, x0 = (ch & 7), sw = (c >> 2) & 1;
-        const uint32_t rowa = dst + blk * 16384 + r * 128;
-        sts128(rowa + (((x0 + sw) ^ (r & 7)) << 4), sw ? hi : lo);
-        sts128(rowa + (((x0 + 1 - sw) ^ (r & 7)) << 4), sw ? lo : hi);
-      }
-      fence_proxy_async_smem();
-      __syncwarp();
-    };
-    auto factors = [&](int j, int code, int ref, __half2 (&m)[2]) {
+    // K and V of a tile by one piece of code (the two roles' loops together are near what the
+    // instruction cache holds: with a copy each the kernel was CONVOLD us, with one CONVNEW): its
+    // rows become FP16 in shared memory, and each register is loaded for the next half step as soon as it
+    // is used.
+    bool ok = true;
+    for (int h = 0; h < 2 * nj; ++h) {
+      const int op = h & 1, j = h >> 1, st = j & 1, use = j >> 1, tok = span.token(v0 + j) + 32 * cw;
+      const int ref = op ? vref : kref, code = op ? l_vs : l_ks;
+      __half2 m[2];
+      bool held[2];
 #pragma unroll
       for (int g = 0; g < 2; ++g) {
         const int e = __shfl_sync(0xffffffffu, code, 2 * (j & 15) + g);
+        held[g] = __shfl_sync(0xffffffffu, l_page, 2 * (j & 15) + g) >= 0;
         m[g] = __float2half2_rn(pow2f(max(-24, e - ref + kUp)));
       }
-    };
-    bool ok = true;
-    for (int j = 0; j < nj; ++j) {
-      const int st = j & 1, use = j >> 1, tok = span.token(v0 + j);
-      const bool edge = bad_pages || !all_visible(p, tok, kPrefillTile, p_lo, p_hi);
-      __half2 mk[2], mv[2];
-      const bool held[2] = {__shfl_sync(0xffffffffu, l_page, 2 * (j & 15)) >= 0, __shfl_sync(0xffffffffu, l_page, 2 * (j & 15) + 1) >= 0};
-      factors(j, l_ks, kref, mk);
-      factors(j, l_vs, vref, mv);
-      if (use > 0 && !__all_sync(0xffffffffu, mbar_wait(BAR(KEMPTY + st), (use - 1) & 1, abort, kPfWaitNs))) { ok = false; break; }
-      store(sb + L::OFF_K + st * L::TILE, uk, mk, edge, tok, held);
-      if (lane == 0) mbar_arrive(BAR(KFULL + st));
-      if (j + 1 < nj) {
-        if (((j + 1) & 15) == 0) batch(j + 1);
-        load(p.k, j + 1, uk);
+      if (use > 0 && !__all_sync(0xffffffffu, mbar_wait(BAR(KEMPTY + 4 * op + st), (use - 1) & 1, abort, kPfWaitNs))) {
+        ok = false;
+        break;
       }
-      if (use > 0 && !__all_sync(0xffffffffu, mbar_wait(BAR(VEMPTY + st), (use - 1) & 1, abort, kPfWaitNs))) { ok = false; break; }
-      store(sb + L::OFF_V + st * L::TILE, uv, mv, edge, tok, held);
-      if (lane == 0) mbar_arrive(BAR(VFULL + st));
-      if (j + 1 < nj) load(p.v, j + 1, uv);
+      // rows that no query row sees or whose page is not of the pool become zero (their codes
+      // may be NaN)
+      if (bad_pages || !all_visible(p, tok - 32 * cw, kPrefillTile, p_lo, p_hi)) {
+#pragma unroll
+        for (int g = 0; g < 2; ++g)
+#pragma unroll
+          for (int i = 0; i < LPR / 2; ++i)
+            if (!held[g] || !any_visible(p, tok + 16 * g + i * RPI + rr, 1, p_lo, p_hi))
+              uk[g * (LPR / 2) + i] = make_uint4(0, 0, 0, 0);
+      }
+      const int jn = min(j + op, nj - 1);  // the next half step's tile (past the end: the last again)
+      if (op && ((j + 1) & 15) == 0) batch(j + 1);
+      const uint32_t dst = sb + (op ? L::OFF_V : L::OFF_K) + st * L::TILE;
+#pragma unroll
+      for (int g = 0; g < 2; ++g) {
+        const uint8_t* at = place(op ? p.k : p.v, jn, g);
+        const __half2 f = m[g];
+#pragma unroll
+        for (int i2 = 0; i2 < LPR / 2; ++i2) {
+          const int i = g * (LPR / 2) + i2, r = 32 * cw + i * RPI + rr;
+          const uint4 u = uk[i];
+          const uint4 lo = make_uint4(hmul2_u32(e4m3x2_to_h2(u.x & 0xFFFFu), f), hmul2_u32(e4m3x2_to_h2(u.x >> 16), f),
+                                      hmul2_u32(e4m3x2_to_h2(u.y & 0xFFFFu), f), hmul2_u32(e4m3x2_to_h2(u.y >> 16), f));
+          const uint4 hi = make_uint4(hmul2_u32(e4m3x2_to_h2(u.z & 0xFFFFu), f), hmul2_u32(e4m3x2_to_h2(u.z >> 16), f),
+                                      hmul2_u32(e4m3x2_to_h2(u.w & 0xFFFFu), f), hmul2_u32(e4m3x2_to_h2(u.w >> 16), f));
+          uk[i] = ldg16_now(at + i2 * RPI * D);
+          // chunks 2c and 2c + 1 of the row; the row's second half writes them in the other
+          // order, so that eight lanes' stores meet all banks
+          const int ch = 2 * c, blk = ch >> 3, x0 = (ch & 7), sw = (c >> 2) & 1;
+          const uint32_t rowa = dst + blk * 16384 + r * 128;
+          sts128(rowa + (((x0 + sw) ^ (r & 7)) << 4), sw ? hi : lo);
+          sts128(rowa + (((x0 + 1 - sw) ^ (r & 7)) << 4), sw ? lo : hi);
+        }
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(BAR(KFULL + 4 * op + st));
     }
     if (!ok && lane == 0) pf_raise(abort);
   } else {
