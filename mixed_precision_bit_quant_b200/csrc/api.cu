@@ -313,7 +313,7 @@ static int check_kv8_shape(const thrift_kv8_shape* s, bool with_q) {
   if (s->dtype != THRIFT_BF16 && s->dtype != THRIFT_FP16) return THRIFT_ERR_INVALID;
   if (with_q && (s->Hq < 1 || s->Hq % s->Hkv != 0)) return THRIFT_ERR_INVALID;
   const long long cap = (long long)s->table_cols * s->page;
-  if (s->max_len > cap || s->max_q > s->n) return THRIFT_ERR_INVALID;
+  if (s->max_len > cap || s->max_q > s->n || (s->n > 0 && s->max_q == 0)) return THRIFT_ERR_INVALID;
   if (cap > (1 << 24) || (long long)s->B * s->Hkv > 65535) return THRIFT_ERR_UNSUPPORTED;
   if (with_q && (long long)s->n * s->Hq > 0x7FFFFFFFLL) return THRIFT_ERR_UNSUPPORTED;
   // 16-token tiles of all sequences, kv heads and tiles of 8 rows are counted in 32 bits
@@ -356,7 +356,7 @@ thrift_status thrift_kv8_append(const thrift_kv8_shape* shape, const thrift_kv8_
   int e = check_kv8_shape(shape, false);
   if (e) return (thrift_status)e;
   if (!kv8_cache_ok(cache) || !aligned4(table) || !aligned4(lens) || !kv8_rows_ok(shape, cu)) return THRIFT_ERR_INVALID;
-  if (shape->n == 0 || shape->max_q == 0) return THRIFT_OK;
+  if (shape->n == 0) return THRIFT_OK;
   const int64_t row = (int64_t)shape->Hkv * shape->d;
   if (!aligned16(k) || !aligned16(v) || k_stride < row || v_stride < row || k_stride % 8 != 0 || v_stride % 8 != 0)
     return THRIFT_ERR_INVALID;
@@ -372,7 +372,7 @@ static int check_kv8_mask(const thrift_kv8_mask* m) {
 }
 
 size_t thrift_kv8_attn_workspace_bytes(const thrift_kv8_shape* shape, const thrift_kv8_mask* mask, int with_w) {
-  if (check_kv8_shape(shape, true) != 0 || check_kv8_mask(mask) != 0 || shape->n == 0 || shape->max_q == 0) return 0;
+  if (check_kv8_shape(shape, true) != 0 || check_kv8_mask(mask) != 0 || shape->n == 0) return 0;
   return kv8_attn_workspace(*shape, *mask, with_w != 0);
 }
 
@@ -386,7 +386,7 @@ thrift_status thrift_kv8_attn(const thrift_kv8_shape* shape, const thrift_kv8_ma
   if (!kv8_cache_ok(cache) || !aligned4(table) || !aligned4(lens) || !kv8_rows_ok(shape, cu) || !null_or_aligned4(lse))
     return THRIFT_ERR_INVALID;
   if (w != nullptr && (!aligned16(w) || w_cols < shape->max_len)) return THRIFT_ERR_INVALID;
-  if (shape->n == 0 || shape->max_q == 0) return THRIFT_OK;
+  if (shape->n == 0) return THRIFT_OK;
   if (!aligned16(q) || !aligned16(o) || q_stride < (int64_t)shape->Hq * shape->d || q_stride % 8 != 0)
     return THRIFT_ERR_INVALID;
   const size_t need = kv8_attn_workspace(*shape, *mask, w != nullptr);

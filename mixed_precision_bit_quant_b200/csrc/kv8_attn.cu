@@ -208,6 +208,13 @@ __device__ __forceinline__ Share find_share(const AttnParams& p, int B) {
   return found;
 }
 
+// Where a segment's state goes, besides a slot of the workspace.
+constexpr long long kWhole = -1, kToCluster = -2;
+// Shared memory in floats: the warps' outputs, their maxima and sums, then (for a cluster) the
+// CTA's own.
+__host__ __device__ constexpr int cluster_ml_at(int d, int nt) { return kSplitWarps * 8 * nt * (d + 4 + 2); }
+__host__ __device__ constexpr int split_smem(int d, int nt) { return 4 * (cluster_ml_at(d, nt) + 8 * nt * 2); }
+
 // Each warp walks its own tiles of 16 tokens straight from global memory into matrix
 // fragments -- the codes' layout in a page is the fragments' layout, so nothing is staged --
 // with the next tile's loads in flight, and keeps its own softmax state; the warps' states are
@@ -218,13 +225,10 @@ __device__ __forceinline__ Share find_share(const AttnParams& p, int B) {
 // e_ref the largest seen, so the products see bare codes; S's fragment becomes P's by one
 // 8x8 transpose.  A row's maximum is raised (and O rescaled) only when a logit
 // exceeds it by 4 binades: the common step needs one vote and no cross-lane maximum.
-// Where a segment's state goes, besides a slot of the workspace.
-constexpr long long kWhole = -1, kToCluster = -2;
-// Shared memory in floats: the warps' outputs, their maxima and sums, then (for a cluster) the
-// CTA's own.
-__host__ __device__ constexpr int cluster_ml_at(int d, int nt) { return kSplitWarps * 8 * nt * (d + 4 + 2); }
-__host__ __device__ constexpr int split_smem(int d, int nt) { return 4 * (cluster_ml_at(d, nt) + 8 * nt * 2); }
-
+//   Bound by HBM at 8 rows (8 sequences of 32768 tokens, 4 heads a group: 95 us, 5.6 TB/s); at 16
+// rows a step's own latencies bind (two passes of 16 rows over 8 x 16384 tokens: 74 us against 26
+// for the bytes; one pass of 32 rows with the codes in a shared-memory ring took 67, but the ring cost
+// the 8-row case 20 us).
 template <int D, int NT>
 __device__ __forceinline__ void split_segment(const AttnParams& p, const Seq& s, int b, int hk, int rt, const Span<kTile>& span,
                                               int v0, int v1, long long slot, float* sm) {
@@ -516,7 +520,8 @@ __global__ void __launch_bounds__(kSplitThreads, resident_ctas(D, NT)) split_ker
 // A short unit (few tiles, and few units): one cluster of eight CTAs takes it, an eighth of its
 // tiles each, and joins the states through the cluster's shared memory -- no search for the
 // shares, no workspace, no second launch.  At one sequence of 517 tokens and 12 heads of 64
-// CLUS1; at four windows of 4096 tokens CLUS2 (split_kernel and merge_kernel first).
+// 5.3 us where split_kernel and merge_kernel take 6.5 + 3.1; at four windows of 4096 tokens 14.3
+// where they take 15.7 + 3.6.
 constexpr int kCluster = 8;
 __device__ __forceinline__ uint32_t peer_address(uint32_t addr, uint32_t rank) {
   uint32_t r;
@@ -672,7 +677,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps) merge_kernel(const AttnParam
 // a thread adds up one token's rows with their final log-sum-exp.  Storing the logits costs
 // 8 bytes a row and token, a fraction of the token's 2 D bytes of codes (4 rows and D = 128:
 // 1/8); computing them again took as long as the attention itself (75 us of 142 at 32
-// sequences of up to 8191 tokens, against LWUS).  One thread adds a token's rows in order: the sum does
+// sequences of up to 8191 tokens, against 8).  One thread adds a token's rows in order: the sum does
 // not depend on how the work was spread.
 constexpr int kWeightRows = 64;  // the most rows of split_kernel
 constexpr int kWeightThreads = 256;

@@ -12,7 +12,15 @@
 //              alternate, so that one tile's products run under the other's exponentials
 // The products need one type for both operands: e4m3 codes are exact in FP16, with a
 // page's scale relative to the largest of the run (2^(e - e_ref), exact down to 2^-24, that is
-// for pages up to 2^21 smaller); the query enters as FP16 scaled by a power of two per row.
+// for pages up to 2^21 smaller); the query enters as FP16 scaled by a power of two per row tile.
+// 4096 queries over 16389 tokens (32 heads of 128, 4 a kv head): 987 us, 975 TFLOP/s.  No pipe
+// bounds it (of a busy SM's clocks the tensor cores work 57 %, the special-function unit 58 %, the
+// ALUs 46 %): a step's chain of waits does -- S to registers, maximum, exponentials, P to tensor
+// memory, two products -- of which two row tiles keep two in flight and tensor memory holds no third.
+// Without its exponentials it takes 968 us, without the conversion 1004, with an eighth of the
+// products 899, without all three 805.  Tried: exp2 on the FMA pipe for an eighth to a half of the
+// pairs (1051 to 1256: issue slots), two threads a row (1225), persistent CTAs with equal shares of
+// the steps instead of a CTA a unit (1140: longer steps, 30,000 clocks around a piece).
 #include "kv8_attn.cuh"
 
 namespace thrift {
@@ -302,7 +310,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const AttnParams
     regs_dec<kPfConvRegs>();
     // -------------------------------------------------------------- converters
     // K and V of a tile by one piece of code (the two roles' loops together are near what the
-    // instruction cache holds: with a copy each the kernel was CONVOLD us, with one CONVNEW): its
+    // instruction cache holds: windowed prompts of 4096 took 120 us with a copy each, 117 with one): its
     // rows become FP16 in shared memory, and each register is loaded for the next half step as soon as it
     // is used.
     bool ok = true;
@@ -553,7 +561,9 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const AttnParams
 //              by bulk copies, and the rows' scales and log-sum-exps
 //   warp 9     tensor-memory allocator and issuer
 // Two CTAs an SM: the exponentials of one run under the other's waits.  Making the images here,
-// once per token tile, took 368 us where this takes TWUS (2 x 1024 new tokens of 4096, 32 heads).
+// once per token tile, took 368 us where this takes 115 (1996 new tokens of two sequences of 4096
+// and 1933, 32 heads).  Bound by the exponentials (16 a clock and SM) and, next, by the waits of
+// 1.3 waves of CTAs.
 // ---------------------------------------------------------------------------
 // The rows' numbers lie in six slots: when warp 8 fills tile j's, product j - 2 has completed,
 // so S of tile j - 4 was read and tile j - 6, the slot's last, is done with.

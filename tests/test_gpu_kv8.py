@@ -506,6 +506,38 @@ def test_captured_calls_read_lengths_when_they_run():
         assert dl.tolist() == [min(x, 48) for x in n]
 
 
+def test_a_captured_chunk_reads_lengths_when_it_runs():
+    """Chunks of several tokens under a window, with sums, captured once: the tile kernels."""
+    B, Hq, Hkv, d, page, cap, n = 2, 16, 2, 64, 32, 16, 60
+    cache = mq.kv8_alloc(B * cap, Hkv, page, d, "cuda")
+    table = np.random.default_rng(0).permutation(B * cap).reshape(B, cap)
+    _fill(cache, table, [cap * page] * B, 3)
+    cache.ks.fill_(121), cache.vs.fill_(120)
+    t, lens, cu = _i32(table), _i32([40, 20]), _i32([0, 40, 60])
+    q = torch.zeros((n, Hq, d), dtype=torch.float16, device="cuda")
+    w = torch.zeros((B, Hkv, cap * page), device="cuda")
+    o, lse = torch.zeros_like(q), torch.zeros((n, Hq), device="cuda")
+    ws = torch.empty(mq.kv8_attention_workspace(q, cache, t, lens, cu=cu, max_q=50, window=100, sinks=3, weights=w),
+                     dtype=torch.uint8, device="cuda")
+
+    def call():
+        mq.kv8_attention(q, cache, t, lens, cu=cu, max_q=50, window=100, sinks=3, weights=w, o=o, lse=lse, ws=ws)
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        call()
+    s.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    g = torch.Generator().manual_seed(0)
+    for ln, c in (([40, 20], [0, 40, 60]), ([500, 300], [0, 50, 60]), ([333, 512], [0, 12, 60])):
+        lens.copy_(_i32(ln)), cu.copy_(_i32(c)), q.copy_(torch.randn(q.shape, generator=g)), w.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        ref = kv8.attend(_np(cache), q.double().cpu().numpy(), table, ln, c, 100, 3)
+        _check(o, lse, w, np.zeros(w.shape), ref, d, max(ln), "fp16")
+
+
 def test_calls_on_two_streams_at_once():
     """Two streams, each with its own workspace, against the same calls one after the other."""
     page, Hkv, Hq, d = 64, 8, 32, 128

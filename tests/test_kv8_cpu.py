@@ -50,7 +50,7 @@ def test_cache_bytes():
 
 
 SHAPES = [(dict(B=0), INVALID), (dict(table_cols=0), INVALID), (dict(n=-1), INVALID), (dict(max_len=0), INVALID),
-          (dict(max_len=257), INVALID), (dict(max_q=3), INVALID), (dict(dtype=2), INVALID), (dict(d=96), UNSUPPORTED),
+          (dict(max_len=257), INVALID), (dict(max_q=3), INVALID), (dict(max_q=0), INVALID), (dict(dtype=2), INVALID), (dict(d=96), UNSUPPORTED),
           (dict(page=48), UNSUPPORTED), (dict(page=8, max_len=8), UNSUPPORTED), (dict(Hkv=0), INVALID),
           (dict(B=32768, Hkv=2, n=32768), UNSUPPORTED), (dict(table_cols=(1 << 18) + 1), UNSUPPORTED)]
 
