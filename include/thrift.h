@@ -389,8 +389,9 @@ THRIFT_API thrift_status thrift_kv8_append(const thrift_kv8_shape *shape, const 
  * the call adds, for every visible token, the attention weights that the
  * group's query rows gave it: w[b][h][t] += sum exp(s - lse), in a fixed order.
  * Logits, softmax statistics and sums are FP32; q enters the products as FP16
- * after an exact power-of-two scaling per row, the probabilities as FP16 (11
- * bits; scaled so that those above 2^-25 of the largest are normal numbers).
+ * after an exact power-of-two scaling (per row, or per tile of 128 rows for more
+ * than 64 rows of a kv head), the probabilities as FP16 (11 bits; scaled so that
+ * those above 2^-25, there 2^-23, of the largest are normal numbers).
  * ws: thrift_kv8_attn_workspace_bytes bytes (16-byte aligned; NULL if 0).  Calls
  * whose work can overlap on the GPU need their own.
  */

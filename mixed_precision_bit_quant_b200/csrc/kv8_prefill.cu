@@ -14,13 +14,14 @@
 // page's scale relative to the largest of the run (2^(e - e_ref), exact down to 2^-24, that is
 // for pages up to 2^21 smaller); the query enters as FP16 scaled by a power of two per row tile.
 // 4096 queries over 16389 tokens (32 heads of 128, 4 a kv head): 987 us, 975 TFLOP/s.  No pipe
-// bounds it (of a busy SM's clocks the tensor cores work 57 %, the special-function unit 58 %, the
-// ALUs 46 %): a step's chain of waits does -- S to registers, maximum, exponentials, P to tensor
-// memory, two products -- of which two row tiles keep two in flight and tensor memory holds no third.
-// Without its exponentials it takes 968 us, without the conversion 1004, with an eighth of the
-// products 899, without all three 805.  Tried: exp2 on the FMA pipe for an eighth to a half of the
-// pairs (1051 to 1256: issue slots), two threads a row (1225), persistent CTAs with equal shares of
-// the steps instead of a CTA a unit (1140: longer steps, 30,000 clocks around a piece).
+// bounds it: at 2048 queries over 4096 tokens the tensor cores work 42 % of the clocks in the mean
+// over the SMs (56 % on the busiest), the special-function unit 42 %, the ALUs 35 %.  A step's chain
+// of waits does -- S to registers, maximum, exponentials, P to tensor memory, two products -- of
+// which two row tiles keep two in flight; tensor memory holds no third.  Copies that skip work, at
+// 990 us with all of it: no exponentials 968, no conversion 1004, an eighth of Q K^T and a quarter of
+// P V 899, all three left out so 805.  Tried and slower: exp2 on the FMA pipe (1085, 1177 and 1256 us for 1, 3
+// and 4 of 8 pairs, against 1051 for that build without), two threads a row (1225 against 990),
+// persistent CTAs with equal shares of the steps (1140 to 1230 against 990).
 #include "kv8_attn.cuh"
 
 namespace thrift {
