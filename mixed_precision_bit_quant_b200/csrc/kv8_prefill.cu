@@ -13,7 +13,8 @@
 // The products need one type for both operands: e4m3 codes are exact in FP16, with a
 // page's scale relative to the largest of the run (2^(e - e_ref), exact down to 2^-24, that is
 // for pages up to 2^21 smaller); the query enters as FP16 scaled by a power of two per row tile.
-// 4096 queries over 16389 tokens (32 heads of 128, 4 a kv head): 987 us, 975 TFLOP/s.  No pipe
+// 4096 queries over 16389 tokens (32 heads of 128, 4 a kv head): 987 us, 975 TFLOP/s, in repeated
+// calls (1015 us, 948 TFLOP/s, in turn with other work).  No pipe
 // bounds it: at 2048 queries over 4096 tokens the tensor cores work 42 % of the clocks in the mean
 // over the SMs (56 % on the busiest), the special-function unit 42 %, the ALUs 35 %.  A step's chain
 // of waits does -- S to registers, maximum, exponentials, P to tensor memory, two products -- of
