@@ -417,8 +417,9 @@ THRIFT_API thrift_status thrift_kv8_attn(const thrift_kv8_shape *shape, const th
  * written twice); a destination page's e is the largest of its tokens' source
  * pages', codes rounded again as by append; slots past the last kept token are
  * left as they were.  dst_lens [B] gets the lengths, dst_w [B][Hkv][dst_w_cols]
- * the kept tokens' w followed by zeros (it must not overlap w), kept
- * [B][Hkv][keep] their old positions followed by -1.  Positions are renumbered:
+ * the kept tokens' w followed by zeros, kept [B][Hkv][keep] their old positions
+ * followed by -1.  No output may overlap an input (dst_lens over lens and dst_w
+ * over w give THRIFT_ERR_INVALID).  Positions are renumbered:
  * a later window counts kept tokens.  w must not hold NaN; w_cols >= max_len,
  * dst_cols * page >= min(keep, max_len) <= dst_w_cols.
  */

@@ -627,7 +627,7 @@ def kv8_evict(cache: Kv8Cache, table: torch.Tensor, lens: torch.Tensor, weights:
     """thrift_kv8_evict: copy every sequence's and kv head's `keep` tokens with the largest weights (the first
     `sinks` and the last `recent` always among them) to the pages dst_table of dst -> (dst_lens int32 [B], kept
     int32 [B, Hkv, keep], the old positions, -1 past the last).  dst may be `cache` if its pages dst_table are
-    none that the call reads; dst_weights must not overlap weights."""
+    none that the call reads; dst_weights must not overlap weights, nor dst_lens lens."""
     _want_kv8(cache, "cache")
     _want_kv8(dst, "dst")
     dev, Hkv = cache.device, cache.Hkv
@@ -652,6 +652,8 @@ def kv8_evict(cache: Kv8Cache, table: torch.Tensor, lens: torch.Tensor, weights:
         lens_ptr = dst_lens.data_ptr()
     else:
         lens_ptr = _kv8_ints(dst_lens, "dst_lens", (B,), dev)
+        if -4 * B < lens_ptr - lp < 4 * B:
+            raise ValueError("dst_lens: must not overlap lens")
     if kept is None:
         kept = torch.empty((B, Hkv, max(keep, 0)), dtype=torch.int32, device=dev)
         kept_ptr = kept.data_ptr()

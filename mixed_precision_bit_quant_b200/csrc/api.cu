@@ -345,6 +345,11 @@ static Kv8Args kv8_args(const thrift_kv8_shape* s, const thrift_kv8_cache* c, co
   return a;
 }
 
+static bool overlap(const void* a, int64_t na, const void* b, int64_t nb) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + (uintptr_t)nb && y < x + (uintptr_t)na;
+}
+
 // cu NULL stands for one new token per sequence.
 static bool kv8_rows_ok(const thrift_kv8_shape* s, const int32_t* cu) {
   return cu != nullptr ? null_or_aligned4(cu) : (s->n == s->B && s->max_q >= 1);
@@ -411,6 +416,10 @@ thrift_status thrift_kv8_evict(const thrift_kv8_shape* shape, const thrift_kv8_c
   if (keep < 1 || sinks < 0 || recent < 0 || (int64_t)sinks + recent > keep) return THRIFT_ERR_INVALID;
   const int64_t most = keep < shape->max_len ? keep : shape->max_len;
   if (w_cols < shape->max_len || dst_w_cols < most || dst_cols < 1 || (int64_t)dst_cols * shape->page < most)
+    return THRIFT_ERR_INVALID;
+  // every kv head reads its sequence's length and weights, one writes the new length
+  const int64_t heads = (int64_t)shape->B * shape->Hkv;
+  if (overlap(lens, 4LL * shape->B, dst_lens, 4LL * shape->B) || overlap(w, 4 * heads * w_cols, dst_w, 4 * heads * dst_w_cols))
     return THRIFT_ERR_INVALID;
   Kv8Evict v;
   v.w = w; v.w_cols = w_cols; v.dst_w_cols = dst_w_cols;

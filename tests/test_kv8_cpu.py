@@ -35,7 +35,7 @@ def _append(shape=None, cache=None, k=16, ks=256, v=16, vs=256, table=16, lens=1
 
 
 def _evict(shape=None, cache=None, table=16, lens=16, w=16, w_cols=256, keep=64, sinks=4, recent=8, dst=None,
-           dst_table=16, dst_cols=1, dst_lens=16, dst_w=16, dst_w_cols=64, kept=16):
+           dst_table=16, dst_cols=1, dst_lens=1 << 20, dst_w=1 << 21, dst_w_cols=64, kept=1 << 22):
     s, c, e = shape or _shape(), cache or _cache(), dst or _cache()
     return mq.lib().thrift_kv8_evict(ctypes.byref(s), ctypes.byref(c), table, lens, w, w_cols, keep, sinks, recent,
                                      ctypes.byref(e), dst_table, dst_cols, dst_lens, dst_w, dst_w_cols, kept, None)
@@ -96,7 +96,10 @@ def test_bad_append_arguments(kw):
                                 dict(sinks=60, recent=5), dict(sinks=2 ** 31 - 1, recent=2 ** 31 - 1),
                                 dict(dst=_cache(0)), dict(dst=_cache(v=24)), dict(dst_table=None), dict(dst_cols=0),
                                 dict(keep=65, dst_cols=1), dict(dst_w_cols=63), dict(dst_w=None), dict(dst_lens=None),
-                                dict(kept=None), dict(kept=18), dict(dst_w=24)])
+                                dict(kept=None), dict(kept=18), dict(dst_w=(1 << 21) + 8),
+                                # outputs over inputs that other CTAs still read
+                                dict(dst_lens=16), dict(dst_lens=20), dict(lens=1 << 20, dst_lens=(1 << 20) - 4),
+                                dict(dst_w=16), dict(dst_w=16 + 4 * 256), dict(w=1 << 21, dst_w=(1 << 21) - 64)])
 def test_bad_evict_arguments(kw):
     assert _evict(**kw) == INVALID
 
@@ -175,6 +178,8 @@ def test_binding_refuses_append_and_evict(any_device):
     w, dw = torch.zeros((2, 2, 48)), torch.zeros((2, 2, 16))
     with pytest.raises(ValueError, match="overlap"):
         mq.kv8_evict(c, t, n, w, c, t, w, 16)
+    with pytest.raises(ValueError, match="dst_lens"):
+        mq.kv8_evict(c, t, n, w, c, t, dw, 16, dst_lens=n)
     with pytest.raises(ValueError, match="dst"):
         mq.kv8_evict(c, t, n, w, _args(page=32)["cache"], t, dw, 16)
     with pytest.raises(ValueError, match="kept"):
