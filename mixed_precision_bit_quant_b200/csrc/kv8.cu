@@ -122,19 +122,28 @@ struct SelectParams {
   int Hkv, keep, sinks, recent, max_len;
 };
 
-// FP32 -> unsigned that orders like the value (-0 counts as 0).
+// FP32 -> unsigned that orders like the value (-0 counts as 0), within [1, 2^32 - 2]: a token past
+// the end has kNone, one that stays in any case kForced.
+constexpr uint32_t kNone = 0u, kForced = 0xFFFFFFFFu;
 __device__ __forceinline__ uint32_t order_key(float x) {
   const uint32_t b = __float_as_uint(x + 0.0f);
-  return b ^ ((b >> 31) ? 0xFFFFFFFFu : 0x80000000u);
+  return min(max(b ^ ((b >> 31) ? 0xFFFFFFFFu : 0x80000000u), kNone + 1), kForced - 1);
+}
+__device__ __forceinline__ float key_value(uint32_t k) {
+  return __uint_as_float(k ^ ((k >> 31) ? 0x80000000u : 0xFFFFFFFFu));
 }
 
-// One CTA per (sequence, kv head).  The free tokens are [lo, hi) (between the sinks and the
-// recent ones); `want` of them stay.  Three passes of 11, 11 and 10 bits of the key narrow
-// the want-th largest key down to one value; tokens above it stay, and of those equal to it
-// the first ones.  A warp takes a contiguous share of the tokens, so that it can count and
-// write its kept ones in order; up to 32 KEYS tokens a warp (max_len <= 1024 KEYS) their keys are
-// loaded once and stay in registers (at 64 heads of up to 32768 tokens 43 us when every pass
-// loaded them again, now 27).
+// One CTA per (sequence, kv head).  Sinks and recent tokens carry the highest key, so that the
+// `keep` largest keys stay.  Three passes of 11, 11 and 10 bits of the key narrow the keep-th largest
+// down to one value; tokens above it stay, and of those equal to it the first ones.  A warp
+// takes a contiguous share of the tokens, so that it can count and write its kept ones in order; up
+// to 32 KEYS tokens a warp (max_len <= 1024 KEYS) their keys are loaded once and stay in registers
+// (at 64 heads of up to 32768 tokens 43 us when every pass loaded them again, 27 with them).
+//   A lane holds four neighbours of each 128 tokens: 16-byte loads where the rows of w allow them,
+// and one running count for four tokens (with single tokens 27 us, of whose 54,000 clocks a CTA the
+// final pass took 17,000: ballots and bit counts; now 21).  A CTA is bound by its own instructions
+// and latencies.  With single tokens, clusters of 4 CTAs a head that joined their histograms through
+// shared memory took 22 us, four copies of the histogram 28.
 template <int KEYS>
 __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const SelectParams p) {
   __shared__ uint32_t hist[2048];
@@ -161,34 +170,61 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const SelectP
     return;
   }
   const int lo = p.sinks, hi = n - p.recent;  // keep >= sinks + recent and n > keep: lo < hi
-  const int steps = (n + kSelThreads - 1) / kSelThreads, w0 = warp * steps * 32 + lane;  // this lane's tokens: w0 + 32 i
-  float x[KEYS > 0 ? KEYS : 1];
+  // this lane's tokens: w0 + 128 i + 0 .. 3
+  const int steps = (n + 4 * kSelThreads - 1) / (4 * kSelThreads), w0 = warp * steps * 128 + 4 * lane;
+  const bool vec = p.w_cols % 4 == 0;
+  // Tokens past the end take values of the same row, which have no effect.
+  auto load = [&](int t, uint32_t (&k)[4]) {
+    if (vec) {
+      const uint4 u = ldg16_now(w + min((long long)t, p.w_cols - 4));
+      k[0] = u.x; k[1] = u.y; k[2] = u.z; k[3] = u.w;
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) k[e] = __float_as_uint(ldg4_now(w + min(t + e, n - 1)));
+    }
+  };
+  auto to_keys = [&](int t, uint32_t (&k)[4]) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const bool free = t + e >= lo && t + e < hi;
+      k[e] = free ? order_key(__uint_as_float(k[e])) : t + e < n ? kForced : kNone;
+    }
+  };
+  constexpr int Q = KEYS > 0 ? KEYS / 4 : 1;
+  uint32_t key[Q][4];
   if constexpr (KEYS > 0) {
 #pragma unroll
-    for (int i = 0; i < KEYS; ++i) x[i] = ldg4_now(w + min(w0 + 32 * min(i, steps - 1), n - 1));
+    for (int i = 0; i < Q; ++i) load(w0 + 128 * min(i, steps - 1), key[i]);
+#pragma unroll
+    for (int i = 0; i < Q; ++i) to_keys(w0 + 128 * i, key[i]);
   }
-  auto each = [&](auto&& f) {  // f(token, weight) for this lane's tokens, in step with the warp
+  auto each = [&](auto&& f) {  // f(first token, keys) for this lane's tokens, in step with the warp
     if constexpr (KEYS > 0) {
 #pragma unroll
-      for (int i = 0; i < KEYS; ++i) {
+      for (int i = 0; i < Q; ++i) {
         if (i >= steps) break;
-        f(w0 + 32 * i, x[i]);
+        f(w0 + 128 * i, key[i]);
       }
     } else {
 #pragma unroll 4
-      for (int i = 0; i < steps; ++i) f(w0 + 32 * i, __ldg(w + min(w0 + 32 * i, n - 1)));
+      for (int i = 0; i < steps; ++i) {
+        uint32_t k[4];
+        load(w0 + 128 * i, k);
+        to_keys(w0 + 128 * i, k);
+        f(w0 + 128 * i, k);
+      }
     }
   };
-  uint32_t left = (uint32_t)(m - p.sinks - p.recent), prefix = 0;
-  const bool any = left > 0;
-  for (int pass = 0; any && pass < 3; ++pass) {
+  uint32_t left = (uint32_t)m, prefix = 0;
+  for (int pass = 0; pass < 3; ++pass) {
     const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0), bits = pass == 2 ? 10 : 11;
+    const uint32_t high = pass == 0 ? 0u : ~0u << (shift + bits);
     hist[tid] = hist[tid + 1024] = 0;
     __syncthreads();
-    each([&](int t, float v) {
-      const uint32_t k = order_key(v);
-      if (t >= lo && t < hi && (pass == 0 || (k >> (shift + bits)) == (prefix >> (shift + bits))))
-        atomicAdd(&hist[(k >> shift) & ((1u << bits) - 1u)], 1u);
+    each([&](int, const uint32_t (&k)[4]) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (((k[e] ^ prefix) & high) == 0 && k[e] != kNone) atomicAdd(&hist[(k[e] >> shift) & ((1u << bits) - 1u)], 1u);
     });
     __syncthreads();
     // the bin that holds the left-th largest: suffix sums, two bins a thread
@@ -213,17 +249,16 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const SelectP
     left = s_left;
   }
   // the threshold key is `prefix`, of which the first `left` tokens stay
-  auto above = [&](int t, uint32_t k) -> bool { return t < lo || t >= hi || (any && k > prefix); };
   uint32_t cnt = 0, ties = 0;
-  each([&](int t, float v) {
-    const uint32_t k = order_key(v);
-    const bool a = above(t, k);
-    cnt += t < n && a;
-    ties += t < n && !a && any && k == prefix;
+  each([&](int, const uint32_t (&k)[4]) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      cnt += k[e] > prefix;
+      ties += k[e] == prefix;
+    }
   });
   cnt = __reduce_add_sync(0xffffffffu, cnt);
   ties = __reduce_add_sync(0xffffffffu, ties);
-  __syncthreads();
   if (lane == 0) {
     wsum[warp] = cnt;
     wties[warp] = ties;
@@ -233,19 +268,44 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const SelectP
   uint32_t at = __reduce_add_sync(0xffffffffu, lane < warp ? wsum[lane] : 0u);
   uint32_t tie_at = __reduce_add_sync(0xffffffffu, lane < warp ? wties[lane] : 0u);
   at += min(tie_at, left);
-  each([&](int t, float v) {
-    const uint32_t k = order_key(v), below = (1u << lane) - 1u;
-    const bool a = t < n && above(t, k), tie = t < n && !a && any && k == prefix;
-    const uint32_t bt = __ballot_sync(0xffffffffu, tie);
-    const bool stay = a || (tie && tie_at + __popc(bt & below) < left);
-    const uint32_t bs = __ballot_sync(0xffffffffu, stay);
-    if (stay) {
-      const uint32_t r = at + __popc(bs & below);
-      kept[r] = t;
-      dw[r] = v;
+  // how many of 0 .. 4 a lane the lanes before this one have
+  auto before = [&](uint32_t c) -> uint32_t {
+    const uint32_t below = (1u << lane) - 1u;
+    return __popc(__ballot_sync(0xffffffffu, c & 1u) & below) + 2 * __popc(__ballot_sync(0xffffffffu, c & 2u) & below) +
+           4 * __popc(__ballot_sync(0xffffffffu, c & 4u) & below);
+  };
+  each([&](int t, const uint32_t (&k)[4]) {
+    bool stay[4], tie[4];
+    uint32_t c = 0, ct = 0;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      stay[e] = k[e] > prefix;
+      tie[e] = k[e] == prefix;
+      ct += tie[e];
     }
-    at += __popc(bs);
-    tie_at += __popc(bt);
+    if (__any_sync(0xffffffffu, ct != 0)) {
+      const uint32_t first = before(ct);
+      uint32_t r = tie_at + first;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        stay[e] = stay[e] || (tie[e] && r < left);
+        r += tie[e];
+      }
+      tie_at += __shfl_sync(0xffffffffu, first + ct, 31);
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) c += stay[e];
+    const uint32_t first = before(c);
+    uint32_t r = at + first;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      if (stay[e] && r < (uint32_t)p.keep) {  // always below, unless the inputs change under the call
+        kept[r] = t + e;
+        dw[r] = k[e] == kForced ? __ldg(w + t + e) : key_value(k[e]);
+      }
+      r += stay[e];
+    }
+    at += __shfl_sync(0xffffffffu, first + c, 31);
   });
 }
 
@@ -285,8 +345,9 @@ __global__ void __launch_bounds__(kMoveThreads, 6) evict_move_kernel(const MoveP
   int most[2] = {0, 0};
   if ((int)threadIdx.x < cnt) {
     const int t = __ldg(p.kept + ((long long)b * p.Hkv + h) * p.keep + r0 + threadIdx.x);
-    const int pg = __ldg(p.table + (long long)b * p.table_cols + t / p.page);
-    const bool ok = pg >= 0 && pg < p.num_pages;
+    const bool in = t >= 0 && t < n;  // always, unless the inputs change under the call
+    const int pg = __ldg(p.table + (long long)b * p.table_cols + (in ? t / p.page : 0));
+    const bool ok = in && pg >= 0 && pg < p.num_pages;
     if (!ok) raise_bad();
     const long long ph = (long long)pg * p.Hkv + h;
     row[threadIdx.x] = ok ? ph * p.page + t % p.page : -1;

@@ -366,7 +366,8 @@ def _evict_case(Hkv, d, page, lens, keep, sinks, recent, w=None, seed=0, same_po
     (2, 64, 16, [0, 1, 5, 100, 37], 20, 2, 3), (1, 128, 64, [4099], 1024, 4, 128), (8, 128, 128, [300, 299], 299, 0, 0),
     (3, 64, 32, [700, 31], 1, 0, 1), (1, 64, 16, [2000], 7, 0, 0), (2, 128, 16, [50], 64, 4, 4),
     (1, 128, 16, [333], 20, 20, 0), (1, 128, 16, [333], 20, 0, 20), (1, 64, 16, [333], 20, 8, 12),
-    (1, 64, 64, [40000], 9000, 3, 77)])
+    (1, 64, 64, [40000], 9000, 3, 77), (2, 64, 64, [20001, 0, 300, 8193], 3001, 3, 77), (1, 64, 128, [9000], 4000, 4000, 0),
+    (1, 64, 128, [8193, 50], 1, 0, 0), (1, 64, 64, [33000, 100, 0], 12001, 12000, 1)])
 def test_evict(Hkv, d, page, lens, keep, sinks, recent):
     _evict_case(Hkv, d, page, lens, keep, sinks, recent, seed=keep)
     _evict_case(Hkv, d, page, lens, keep, sinks, recent, seed=keep + 1, same_pool=True)
@@ -384,6 +385,16 @@ def test_evict_ties_and_odd_weights(kind):
     if kind == "signs":
         w[w == 0] = torch.where(torch.rand(int((w == 0).sum()), generator=g) < 0.5, 0.0, -0.0)  # -0 equals 0
     _evict_case(2, 64, 32, [n - 37], 1000, 3, 50, w=torch.nn.functional.pad(w, (0, 12)), seed=2)
+
+
+@pytest.mark.parametrize("n", [20000, 33100])
+@pytest.mark.parametrize("kind", ["equal", "few", "close"])
+def test_evict_ties_of_long_sequences(kind, n):
+    """The kept ones of equal weights are the first, wherever in a sequence that several CTAs share they lie."""
+    g = torch.Generator().manual_seed(6)
+    w = {"equal": torch.ones((1, 2, n)), "few": torch.randint(0, 3, (1, 2, n), generator=g).float(),
+         "close": 1 + torch.randint(0, 500, (1, 2, n), generator=g).float() * 2.0 ** -23}[kind]
+    _evict_case(2, 64, 128, [n - 37], 9001, 3, 50, w=torch.nn.functional.pad(w, (0, -n % 128)), seed=2)
 
 
 def test_evict_bad_pages_are_reported():
