@@ -618,7 +618,10 @@ __global__ void __launch_bounds__(kTwThreads, 2) tile_weights_kernel(const AttnP
   }
   __syncthreads();
   const int32_t* trow = p.table + (long long)b * p.table_cols;
-  // K's codes as FP16, each page relative to the largest exponent of the tile's pages
+  // Some row sees the token.  The table's entries of pages that none sees may be stale numbers of
+  // the pool: neither their codes nor their scales are read.
+  auto seen = [&](int tok) { return tok < s.len && any_visible(p, tok, 1, s.pos0, s.len - 1); };
+  // K's codes as FP16, each page relative to the largest exponent of the tile's visible pages
   constexpr int VR = D / 16, ITEMS = 128 * VR / 256;
   uint4 u[ITEMS];
   int ks[ITEMS];
@@ -629,7 +632,7 @@ __global__ void __launch_bounds__(kTwThreads, 2) tile_weights_kernel(const AttnP
       const int it = tid + 256 * i, tok = t0 + it / VR;
       u[i] = make_uint4(0, 0, 0, 0);
       ks[i] = 0;
-      if (tok < s.len) {
+      if (seen(tok)) {
         const int pg = __ldg(trow + (tok >> p.page_log2));
         if (pg >= 0 && pg < p.num_pages) {
           const long long ph = (long long)pg * p.Hkv + hk;
@@ -788,7 +791,7 @@ __global__ void __launch_bounds__(kTwThreads, 2) tile_weights_kernel(const AttnP
     tc_fence_after();
     tmem_dealloc(tmem, 256);
   }
-  if (tid < 128 && t0 + tid < s.len) {
+  if (tid < 128 && seen(t0 + tid)) {
     const int pg = __ldg(trow + ((t0 + tid) >> p.page_log2));
     if (pg >= 0 && pg < p.num_pages) {
       float* w = p.w + (long long)bk * p.w_cols + t0 + tid;
