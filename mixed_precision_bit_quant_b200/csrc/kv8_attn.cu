@@ -699,8 +699,11 @@ __global__ void __launch_bounds__(kWeightThreads) logit_weights_kernel(const Att
     sum[i] = 0.0f;
     was[i] = w[min(t0 + i * kWeightThreads, s.len - 1)];
   }
+  // a row whose tokens all lie on pages outside the pool has the log-sum-exp -inf, as its
+  // logits: it gives no weight (-inf less -inf would be NaN)
   if ((int)threadIdx.x < rows) {
-    lse2[threadIdx.x] = p.lse2[packed_row(p, s, hk, threadIdx.x)];
+    const float x = p.lse2[packed_row(p, s, hk, threadIdx.x)];
+    lse2[threadIdx.x] = x == -INFINITY ? INFINITY : x;
     pos[threadIdx.x] = s.pos0 + threadIdx.x / p.G;
   }
   __syncthreads();

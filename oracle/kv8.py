@@ -14,7 +14,8 @@ gives no formats or interfaces; the serving form is this library's:
   page's new tokens, at least the page's old e if it holds older tokens of the
   sequence, whose codes are then rounded again;
 * attention: the query at position p sees t <= p and, under a window W,
-  only t > p - W or t < sinks; exact softmax; a row that sees nothing gives 0 and -inf;
+  only t > p - W or t < sinks; exact softmax; a row that sees nothing gives 0 and -inf; a token
+  whose page is outside the pool counts as not visible;
 * eviction: the first ``sinks``, the last ``recent`` and the tokens with the
   largest weights (ties: the lower position) stay, in their order.
 
@@ -98,8 +99,10 @@ def attend(pool, q, table, lens, cu, window=0, sinks=0, scale=0.0):
         q0, q1, L = int(cu[b]), int(cu[b + 1]), int(lens[b])
         for h in range(Hkv if q1 > q0 else 0):
             K, V = tokens(pool, "k", table[b], L, h), tokens(pool, "v", table[b], L, h)
+            pages = np.asarray(table[b])[np.arange(L) // pool["k"].shape[2]]
+            held = (pages >= 0) & (pages < pool["k"].shape[0])
             for r in range(q0, q1):
-                see = visible(L - (q1 - q0) + r - q0, L, window, sinks)
+                see = visible(L - (q1 - q0) + r - q0, L, window, sinks) & held
                 for j in range(h * (Hq // Hkv), (h + 1) * (Hq // Hkv)):
                     if not see.any():
                         o[r, j], a[r, j], lse[r, j] = 0.0, 0.0, -math.inf

@@ -1,5 +1,6 @@
 """The paged 8-bit cache's attention and the pages that its rows do not see: entries of pages that a window
-has left behind hold anything.  Bounds as in test_gpu_kv8.py."""
+has left behind hold anything, and pages outside the pool count as not visible -- in the outputs and in the
+weight sums, whatever number of rows picks the kernel.  Bounds as in test_gpu_kv8.py."""
 import numpy as np
 import pytest
 import torch
@@ -66,3 +67,34 @@ def test_entries_of_pages_left_behind_hold_anything(page, d, lens, news, window,
     got = w.cpu().numpy()
     for b, lo, hi in gone:  # not even rounded
         assert np.array_equal(got[b, :, lo:hi], w0[b, :, lo:hi].astype(np.float32))
+
+
+# ------------------------------------------------- pages outside the pool
+@pytest.mark.parametrize("page,d,lens,news,bad", [
+    (16, 64, [1, 40, 20], [1, 1, 1], {0: [0], 1: [1]}),              # a padded slot; one page of three; a cluster a unit
+    (16, 64, [16, 33], [2, 3], {0: [0], 1: [0, 1, 2]}),
+    (64, 128, [7001, 64, 513], [1, 1, 1], {0: [3, 50], 1: [0]}),     # shares of all tiles, joined afterwards
+    (32, 64, [6400, 32], [3, 2], {0: list(range(200)), 1: [0]}),     # nothing is left of either
+    (64, 64, [300, 128, 90], [80, 128, 20], {0: [1], 1: [0, 1]}),    # many rows
+    (16, 128, [1000, 16], [40, 16], {0: [0, 1, 2, 30, 62], 1: [0]}),
+    (128, 64, [300], [300], {0: [0, 1, 2]}),
+])
+@pytest.mark.parametrize("number", [-1, 2 ** 31 - 1])
+def test_pages_outside_the_pool_give_no_weight(page, d, lens, news, bad, number):
+    B, Hq, Hkv = len(lens), 8, 2
+    cols = -(-max(lens) // page)
+    table, P = _tables(lens, page, cols, 5)
+    cache = _pool(P, Hkv, page, d, 5)
+    _fill(cache, table, lens, 5)
+    for b, c in bad.items():
+        table[b, c] = number
+    w0 = _sums(B, Hkv, cols * page, 6)
+    q, cu, o, lse, w = _call(cache, table, lens, news, Hq, w0)
+    assert mq.device_status() == (1, 1 << 16)
+    ref = kv8.attend(_np(cache), q, table, lens, cu)
+    _check(o, lse, w, w0, ref, d, max(lens), "bf16")
+    got = w.cpu().numpy()
+    for b, c in bad.items():
+        for col in c:
+            lo, hi = col * page, min(lens[b], (col + 1) * page)
+            assert np.array_equal(got[b, :, lo:hi], w0[b, :, lo:hi].astype(np.float32))

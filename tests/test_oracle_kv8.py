@@ -93,3 +93,17 @@ def test_eviction_keeps_forced_tokens_and_the_largest_with_the_lowest_first():
         e = dst["vs"][[1] * 16 + [0] * 4, h].astype(int) - 127
         assert np.all(np.abs(old - new) <= np.ldexp(1.0, -10 + e)[:, None] + np.abs(old) * 2.0 ** -4)
         assert np.array_equal(dw[0, h, :20], ww[0, h, ids]) and not dw[0, h, 20:].any()
+
+
+@pytest.mark.parametrize("number", [-1, 4, 2 ** 31 - 1])
+def test_tokens_of_pages_outside_the_pool_are_not_visible(number):
+    pool = _pool(4, 1, 16, 4)
+    q = np.random.default_rng(3).normal(size=(3, 2, 4))
+    r = kv8.attend(pool, q, [[3, number, 1]], [40], [0, 3])
+    short = dict(pool)  # the same tokens without the page, as a sequence of 24
+    for i, p in enumerate((37, 38, 39)):
+        one = kv8.attend(short, q[i:i + 1], [[3, 1]], [p - 15], [0, 1])
+        assert np.allclose(r["o"][i], one["o"][0]) and np.allclose(r["lse"][i], one["lse"][0])
+    assert not r["w"][0, 0, 16:32].any() and np.isclose(r["w"].sum(), 6)
+    r = kv8.attend(pool, q, [[number, number, number]], [40], [0, 3])
+    assert np.all(r["o"] == 0) and np.all(np.isneginf(r["lse"])) and not r["w"].any()
