@@ -136,7 +136,7 @@ __device__ __forceinline__ void tile_logits(const uint4 (&k)[2][D / 64], const u
 }
 
 constexpr float kLazy = 4.0f;  // a row's maximum is raised only when exceeded by 2^4
-constexpr int kPShift = 11;    // P enters FP16 times 2^11: at most 2^(4 + 11) = 2^15
+constexpr float kPShift = 11.0f;  // P enters FP16 times 2^11: at most 2^(4 + 11) = 2^15
 
 // The visible tokens of sequence b, in 16-token tiles, of one kv head: over the tiles of R rows.
 template <int R>
@@ -221,10 +221,12 @@ __host__ __device__ constexpr int split_smem(int d, int nt) { return 4 * (cluste
 // joined at the end of a segment.
 //   S^T = K Q^T (m = tokens, n = rows): the e4m3 codes are exact in FP16; the page's scale,
 // the row's and the softmax's multiply the FP32 logits.
-//   O^T += V^T P^T: P goes to FP16 as p 2^(e_v - e_ref + 11), where e_v is the page's V exponent and
-// e_ref the largest seen, so the products see bare codes; S's fragment becomes P's by one
-// 8x8 transpose.  A row's maximum is raised (and O rescaled) only when a logit
-// exceeds it by 4 binades: the common step needs one vote and no cross-lane maximum.
+//   O^T += V^T P^T: P goes to FP16 as p 2^(e_v - e_r + 11), where e_v is the page's V exponent, so
+// the products see bare codes; S's fragment becomes P's by one 8x8 transpose.  Both the maximum of
+// p and e_r are the row's own: max p 2^e_r is its largest p 2^e_v so far, so that what it sees of
+// small scale is not lost beside pages that it does not see or hardly weighs (one e_r for the tile,
+// the largest e_v, did).  They are raised (and O rescaled) only when a logit, or a logit with its
+// page's scale, exceeds them by 4 binades: the common step needs one vote and no cross-lane maximum.
 //   Bound by HBM at 8 rows (8 sequences of 32768 tokens, 4 heads a group: 95 us, 5.6 TB/s); at 16
 // rows a step's own latencies bind (two passes of 16 rows over 8 x 16384 tokens: 74 us against 26
 // for the bytes; one pass of 32 rows with the codes in a shared-memory ring took 67, but the ring cost
@@ -251,8 +253,6 @@ __device__ __forceinline__ void split_segment(const AttnParams& p, const Seq& s,
     for (int j = 0; j < D / 16; ++j)
 #pragma unroll
       for (int e = 0; e < 4; ++e) acc[n][j][e] = 0.0f;
-  int e_ref = -1000;
-
   const int32_t* trow = p.table + (long long)b * p.table_cols;
   const int page_mask = (1 << p.page_log2) - 1;
   int l_page = -1, l_ks = 0, l_vs = 0;  // lane's tile of the current batch of 32 of this warp's tiles
@@ -289,7 +289,7 @@ __device__ __forceinline__ void split_segment(const AttnParams& p, const Seq& s,
   }
   float fs[NT][2];   // per column 2t, 2t+1: logits' scale without the page's
   int pos[NT][2];    // per column: the query's position
-  float m[NT][2], l[NT][2];
+  float m[NT][2], l[NT][2], er[NT][2];
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
     const int e = scale_query<D>(8 * n + g < r_cnt, p.fp16, qf[n]);
@@ -301,6 +301,7 @@ __device__ __forceinline__ void split_segment(const AttnParams& p, const Seq& s,
       pos[n][x] = c < r_cnt ? s.pos0 + (r_base + c) / p.G : -1;
       m[n][x] = -INFINITY;
       l[n][x] = 0.0f;
+      er[n][x] = 0.0f;
     }
   }
   auto step = [&](int it, Codes<D>& c, int pg, int ksc, int vsc) {
@@ -346,16 +347,14 @@ __device__ __forceinline__ void split_segment(const AttnParams& p, const Seq& s,
           *reinterpret_cast<float2*>(at + 8 * p.logit_w) = make_float2(x[n][2], x[n][3]);
         }
     }
+    const float ev = (float)(vsc - 127);
     bool raise = false;
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
-      for (int y = 0; y < 2; ++y) raise |= fmaxf(x[n][y], x[n][y + 2]) > m[n][y] + kLazy;
-    const int ev = vsc - 127;
-    if (__any_sync(0xffffffffu, raise) || ev > e_ref) {
-      const int e_new = max(ev, e_ref);
-      const float fe = e_ref > -1000 ? pow2f(max(-126, e_ref - e_new)) : 0.0f;
-      e_ref = e_new;
+      for (int y = 0; y < 2; ++y)
+        raise |= fmaxf(x[n][y], x[n][y + 2]) + fmaxf(ev - er[n][y], 0.0f) > m[n][y] + kLazy;
+    if (__any_sync(0xffffffffu, raise)) {
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -365,20 +364,25 @@ __device__ __forceinline__ void split_segment(const AttnParams& p, const Seq& s,
           mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, 8));
           mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, 16));
           const float mn = fmaxf(m[n][y], mm);
-          const float f = m[n][y] == -INFINITY ? 0.0f : ex2_approx(m[n][y] - mn);
+          const float down = m[n][y] == -INFINITY ? -INFINITY : m[n][y] - mn;
+          const float en = mm == -INFINITY ? er[n][y] : fmaxf(er[n][y] + down, ev + (mm - mn));
+          const float f = ex2_approx(down + (er[n][y] - en));
+          l[n][y] *= ex2_approx(down);
           m[n][y] = mn;
-          l[n][y] *= f;
+          er[n][y] = en;
 #pragma unroll
           for (int j = 0; j < D / 16; ++j) {
-            acc[n][j][y] *= f * fe;
-            acc[n][j][y + 2] *= f * fe;
+            acc[n][j][y] *= f;
+            acc[n][j][y + 2] *= f;
           }
         }
     }
-    const float pv = pow2f(max(-126, ev - e_ref + kPShift));
     uint32_t pb[NT][2];
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
+      float pv[2];  // (bounded, so that times the 0 of an unseen token it stays 0)
+#pragma unroll
+      for (int y = 0; y < 2; ++y) pv[y] = ex2_approx(fminf(ev - er[n][y] + kPShift, 126.0f));
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const float mu = m[n][e & 1];
@@ -387,7 +391,7 @@ __device__ __forceinline__ void split_segment(const AttnParams& p, const Seq& s,
       }
 #pragma unroll
       for (int y = 0; y < 2; ++y) {
-        const __half2 h = __floats2half2_rn(x[n][2 * y] * pv, x[n][2 * y + 1] * pv);
+        const __half2 h = __floats2half2_rn(x[n][2 * y] * pv[0], x[n][2 * y + 1] * pv[1]);
         pb[n][y] = movmatrix(*reinterpret_cast<const uint32_t*>(&h));
       }
     }
@@ -435,13 +439,12 @@ __device__ __forceinline__ void split_segment(const AttnParams& p, const Seq& s,
         sml[(warp * R + c) * 2] = m[n][y];
         sml[(warp * R + c) * 2 + 1] = ll;
       }
-      // back to values: 2^(e_ref - 11) in two steps (e_ref may be -127)
-      const float f1 = count > 0 && e_ref > -1000 ? scale_value((uint32_t)(e_ref + 127)) : 0.0f;
-      const float f2 = 1.0f / (1 << kPShift);
+      // back to values: 2^(e_r - 11) in steps (e_r may be below -126)
+      const float f1 = ex2_approx(0.5f * er[n][y]), f2 = 1.0f / (1 << (int)kPShift);
 #pragma unroll
       for (int j = 0; j < D / 16; ++j)
         *reinterpret_cast<float2*>(so + (warp * R + c) * (D + 4) + g * (D / 8) + 2 * j) =
-            make_float2(acc[n][j][y] * f2 * f1, acc[n][j][y + 2] * f2 * f1);
+            make_float2(acc[n][j][y] * f2 * f1 * f1, acc[n][j][y + 2] * f2 * f1 * f1);
     }
   __syncthreads();
   for (int i = threadIdx.x; i < r_cnt * (D / 4); i += kSplitThreads) {
