@@ -388,10 +388,18 @@ THRIFT_API thrift_status thrift_kv8_append(const thrift_kv8_shape *shape, const 
  * w: NULL, or [B][Hkv][w_cols] FP32 running sums (w_cols >= max_len), to which
  * the call adds, for every visible token, the attention weights that the
  * group's query rows gave it: w[b][h][t] += sum exp(s - lse), in a fixed order.
- * Logits, softmax statistics and sums are FP32; q enters the products as FP16
- * after an exact power-of-two scaling (per row, or per tile of 128 rows for more
- * than 64 rows of a kv head), the probabilities as FP16 (11 bits; scaled so that
- * those above 2^-25, there 2^-23, of the largest are normal numbers).
+ * Logits, softmax statistics and sums are FP32.  q enters the products as FP16
+ * after a power-of-two scaling, exact for components down to 2^-28 of the
+ * largest (of the row, or of a tile of 128 rows for more than 64 rows of a kv
+ * head); smaller ones are off by at most 2^-39 of it.  The probabilities enter as
+ * FP16 (11 bits) times their page's V scale: products p 2^e above 2^-25 of the
+ * row's largest are normal numbers, smaller ones are off by at most 2^-36 of it.
+ * For more than 64 rows, where the V scales of the pages that 256 rows see lie
+ * within 2^12 of each other and their K scales within 2^21, p enters without: normal
+ * above 2^-23 of the row's largest, below off by at most 2^-34; where they lie
+ * further apart those rows take the slower way of few rows (only values of pages
+ * with e = -127, below 2^-118, then count as zero beside larger pages).  q must be
+ * finite, logits below 2^21 in magnitude and values of V below 2^88.
  * ws: thrift_kv8_attn_workspace_bytes bytes (16-byte aligned; NULL if 0).  Calls
  * whose work can overlap on the GPU need their own.
  */

@@ -12,7 +12,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libthrift.so")
 SOURCES = ["api.cu", "quantize.cu", "select.cu", "attn_fwd.cu", "decode.cu", "kv8.cu", "kv8_attn.cu", "kv8_prefill.cu", "mma_probe.cu"]
-HEADERS = ["dev.cuh", "kernels.h", "kv8.cuh", "kv8_attn.cuh", os.path.join("..", "..", "include", "thrift.h")]
+HEADERS = ["dev.cuh", "kernels.h", "kv8.cuh", "kv8_attn.cuh", "kv8_split.cuh", os.path.join("..", "..", "include", "thrift.h")]
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",

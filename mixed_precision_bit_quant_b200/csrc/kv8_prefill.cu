@@ -13,6 +13,10 @@
 // The products need one type for both operands: e4m3 codes are exact in FP16, with a
 // page's scale relative to the largest of the run (2^(e - e_ref), exact down to 2^-24, that is
 // for pages up to 2^21 smaller); the query enters as FP16 scaled by a power of two per row tile.
+// A run whose pages' scales lie further apart (K: 2^21; V: 2^12, beyond which small weights on
+// large pages would be lost in P's FP16) is walked as kv8_split.cuh does, where K and P carry each
+// page's scale for itself; only pages of exponent -127 (zeros, and values below 2^-118) may lie
+// further below the others, and count as zero then.
 // 4096 queries over 16389 tokens (32 heads of 128, 4 a kv head): 987 us, 975 TFLOP/s, in repeated
 // calls (1015 us, 948 TFLOP/s, in turn with other work).  No pipe
 // bounds it: at 2048 queries over 4096 tokens the tensor cores work 42 % of the clocks in the mean
@@ -23,7 +27,7 @@
 // P V 899, all three left out so 805.  Tried and slower: exp2 on the FMA pipe (1085, 1177 and 1256 us for 1, 3
 // and 4 of 8 pairs, against 1051 for that build without), two threads a row (1225 against 990),
 // persistent CTAs with equal shares of the steps (1140 to 1230 against 990).
-#include "kv8_attn.cuh"
+#include "kv8_split.cuh"
 
 namespace thrift {
 namespace kv8 {
@@ -36,6 +40,7 @@ constexpr int kUp = 6;          // codes enter FP16 times 2^6: at most 448 * 64 
 constexpr float kPfLazy = 6.0f;  // a row's maximum is raised when exceeded by 2^6
 constexpr float kTiny = 1.17549435e-38f;  // a logit's scale is never 0: -inf times it stays -inf
 constexpr float kPfShift = 9.0f; // P enters FP16 times 2^9: at most 2^15
+constexpr int kNearK = 21, kNearV = 12;  // exponents of a run's pages that lie at most this far apart
 
 enum PfBar : int {
   KFULL = 0, KEMPTY = 2, VFULL = 4, VEMPTY = 6, SFULL = 8,
@@ -49,8 +54,8 @@ struct PfLayout {
   static constexpr int OFF_K = 2 * TILE;      // two stages
   static constexpr int OFF_V = 4 * TILE;      // two stages
   static constexpr int OFF_BAR = 6 * TILE;
-  static constexpr int OFF_MISC = OFF_BAR + 8 * NPFBAR + 8;  // tmem holder, abort, 12 + 8 words of the start
-  static constexpr int BYTES = OFF_MISC + 96;
+  static constexpr int OFF_MISC = OFF_BAR + 8 * NPFBAR + 8;  // tmem holder, abort, 12 + 8 + 8 words of the start
+  static constexpr int BYTES = OFF_MISC + 128;
   // at least 116 KB, so that one CTA (and its 512 TMEM columns) owns an SM
   static constexpr int DYN = (BYTES + 1024 > 116 * 1024) ? BYTES + 1024 : 116 * 1024;
   static constexpr uint32_t S_COL = 0, O_COL = 256;  // S of tile t at 128 t (P over its first half), O at 256 + D t
@@ -114,6 +119,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const AttnParams
   volatile int* abort = reinterpret_cast<volatile int*>(smem + L::OFF_MISC + 4);
   volatile uint32_t* ekey = misc + 2;  // of each of warps 12-15: largest exponents of K and of V, a bad page
   volatile uint32_t* qkey = misc + 14;  // of each softmax warp: its largest |q|, as bits
+  volatile uint32_t* elow = misc + 22;  // of each of warps 12-15: smallest exponents above -127 of K and of V
   if (tid == 0) {
     for (int k = 0; k < NPFBAR; ++k)
       mbar_init(BAR(k), (k >= KFULL && k < KFULL + 2) || (k >= VFULL && k < VFULL + 2) || (k >= PFULL && k < PFULL + 4) ? 4 : 1);
@@ -188,6 +194,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const AttnParams
     }
   } else {
     int ek = 0, ev = 0;
+    uint32_t lk = 255, lv = 255;
     bool bad = false;
     const int per = page_tok < kPrefillTile ? kPrefillTile >> p.page_log2 : 1;  // pages of a tile
     for (int i = tid - 384; i < nj * per; i += 128) {
@@ -198,17 +205,24 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const AttnParams
         bad = true;
         continue;
       }
-      ek = max(ek, (int)__ldg(p.ks + (long long)pg * p.Hkv + hk));
-      ev = max(ev, (int)__ldg(p.vs + (long long)pg * p.Hkv + hk));
+      const int ksc = __ldg(p.ks + (long long)pg * p.Hkv + hk), vsc = __ldg(p.vs + (long long)pg * p.Hkv + hk);
+      ek = max(ek, ksc);
+      ev = max(ev, vsc);
+      if (ksc > 0) lk = min(lk, (uint32_t)ksc);
+      if (vsc > 0) lv = min(lv, (uint32_t)vsc);
     }
     ek = __reduce_max_sync(0xffffffffu, ek);
     ev = __reduce_max_sync(0xffffffffu, ev);
+    lk = __reduce_min_sync(0xffffffffu, lk);
+    lv = __reduce_min_sync(0xffffffffu, lv);
     if (bad) raise_bad();
     bad = __any_sync(0xffffffffu, bad);
     if (lane == 0) {
       ekey[warp - 12] = ek;
       ekey[warp - 8] = ev;
       ekey[warp - 4] = bad;
+      elow[warp - 12] = lk;
+      elow[warp - 8] = lv;
     }
   }
   tc_fence_before();
@@ -217,6 +231,8 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const AttnParams
   const uint32_t tmem = misc[0];
   const int kref = max(max(ekey[0], ekey[1]), max(ekey[2], ekey[3]));
   const int vref = max(max(ekey[4], ekey[5]), max(ekey[6], ekey[7]));
+  const int klow = min(min(elow[0], elow[1]), min(elow[2], elow[3]));
+  const int vlow = min(min(elow[4], elow[5]), min(elow[6], elow[7]));
   const bool bad_pages = (ekey[8] | ekey[9] | ekey[10] | ekey[11]) != 0;
   // The rows as FP16, scaled by a power of two.  The 128 rows of a tile share it (their largest
   // component lands in [2^14, 2^15)), so that a logit's scale is the tile's: a component 2^31
@@ -254,6 +270,20 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const AttnParams
     fence_proxy_async_smem();
   }
   __syncthreads();
+  if (kref - klow > kNearK || vref - vlow > kNearV) {
+    // scales too far apart: four groups of four warps take 8 rows each as split_kernel does
+    if (warp == 12) tmem_dealloc(tmem, 512);
+    constexpr int F = kPrefillTile / kTile, GROUPS = kPfThreads / kSplitThreads;
+    static_assert(GROUPS * split_smem(D, 1) <= L::OFF_BAR, "the groups' shared memory lies over the barriers");
+    const Span<kTile> all{F * span.s_tiles, F * span.a_tile, F * span.count};
+    float* sm = reinterpret_cast<float*>(smem + (tid / kSplitThreads) * split_smem(D, 1));
+    for (int t = tid / kSplitThreads; 8 * t < r_cnt; t += GROUPS) {
+      split_segment<D, 1, true>(p, s, b, hk, rt * (kPrefillRows / 8) + t, all, F * v0, F * (v0 + nj),
+                                p.nsplit > 1 ? kToRun - split : kWhole, sm);
+      split_sync<true>();  // shared memory is free again
+    }
+    return;
+  }
   volatile int never = 0;
 
   if (warp >= 12) {
@@ -325,7 +355,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const AttnParams
       for (int g = 0; g < 2; ++g) {
         const int e = __shfl_sync(0xffffffffu, code, 2 * (j & 15) + g);
         held[g] = __shfl_sync(0xffffffffu, l_page, 2 * (j & 15) + g) >= 0;
-        m[g] = __float2half2_rn(pow2f(max(-24, e - ref + kUp)));
+        m[g] = __float2half2_rn(pow2f(max(-126, e - ref + kUp)));  // (0 below 2^-24)
       }
       if (use > 0 && !__all_sync(0xffffffffu, mbar_wait(BAR(KEMPTY + 4 * op + st), (use - 1) & 1, abort, kPfWaitNs))) {
         ok = false;

@@ -4,9 +4,12 @@ it sees allow, whatever other pages its tile holds.
 Bounds, per element, on top of test_gpu_kv8.py's (d 2^-23 s on a logit, 2^-11 on a probability, half a step of the
 output).  P enters the products as FP16, whose subnormals are off by 2^-25 at most:
 
-* P carries its page's V scale, and the row's largest product u = max p 2^e enters at 2^11 or above: 2^-36 u a token;
+* taken by up to 64 rows, and by more where scales lie far apart: P carries its page's V scale, and the row's
+  largest product u = max p 2^e enters at 2^11 or above: 2^-36 u a token;
+* more than 64 rows and V scales up to 2^12 apart: the largest p enters at 2^9 or above: 2^-34 max p a token, times
+  the token's 2^e.
 
-It acts on codes up to 448.  A logit's own sums are taken relative to s, the row's largest scale * sum |q k|."""
+Each acts on codes up to 448.  A logit's own sums are taken relative to s, the row's largest scale * sum |q k|."""
 import numpy as np
 import pytest
 import torch
@@ -61,7 +64,8 @@ def _reference(pool, q, table, lens, cu, window, sinks, near):
 
 def _run(Hq, Hkv, d, page, lens, news, ke, ve, window=0, sinks=0, dtype="bf16", seed=0, light=0.0, weights=True, zero=()):
     """ke, ve: exponents (plus 127) of a sequence's pages in order, repeated; light: the logits (natural) of the pages
-    whose V is not of the smallest scale, about; zero: pages of zero codes."""
+    whose V is not of the smallest scale, about; zero: pages of zero codes.  K's pages of far larger scale have
+    their values in one channel, where the queries are 0: logits of 2^20 and more would mean nothing in FP32."""
     B, cols = len(lens), -(-max(lens) // page)
     table = np.random.default_rng(seed).permutation(B * cols).reshape(B, cols)
     cache = _pool(B * cols, Hkv, page, d, seed)
@@ -73,6 +77,8 @@ def _run(Hq, Hkv, d, page, lens, news, ke, ve, window=0, sinks=0, dtype="bf16", 
             for f, e in (("k", ke), ("v", ve)):
                 pool[f][pg, :, :m] = e4m3_encode(r.normal(size=(Hkv, m, d)) * 60)
                 pool[f + "s"][pg] = e[c % len(e)]
+            if ke[c % len(ke)] > min(ke) + 12:
+                pool["k"][pg, ..., 1:] &= 0x80
             if light and ve[c % len(ve)] > min(ve):
                 val = light / np.sqrt(d) * (1 + 0.01 * r.normal(size=(Hkv, m, d)))
                 pool["k"][pg, :, :m] = e4m3_encode(np.ldexp(val, 127 - ke[c % len(ke)]))
@@ -85,12 +91,15 @@ def _run(Hq, Hkv, d, page, lens, news, ke, ve, window=0, sinks=0, dtype="bf16", 
         cu.append(cu[-1] + x)
     q = torch.randn((cu[-1], Hq, d), generator=torch.Generator().manual_seed(seed + 2))
     q = (1 + 0.01 * q if light else q).to(DT[dtype])
+    if max(ke) > min(ke) + 12:
+        q[..., 0] = 0
+    many = max(news) * (Hq // Hkv) > 64
+    weights = weights and not many
     w = torch.zeros((B, Hkv, cols * page), device="cuda") if weights else None
     o, lse = mq.kv8_attention(q.cuda(), cache, _i32(table), _i32(lens), cu=_i32(cu), max_q=max(news), window=window,
                               sinks=sinks, weights=w, want_lse=True)
     assert mq.device_status() == (0, 0)
-    live = [x for x in ve if x > 0]
-    many = max(news) * (Hq // Hkv) > 64
+    live = [x for x in ve if x > 0] or [0]
     # (an exponent of -127 marks values below 2^-118, which count as zero beside pages of ordinary scale)
     ro, ob, rl, lb, rw, wb = _reference(pool, q.double().numpy(), table, lens, cu, window, sinks,
                                         many and max(live) - min(live) <= NEAR)
@@ -104,9 +113,10 @@ def _run(Hq, Hkv, d, page, lens, news, ke, ve, window=0, sinks=0, dtype="bf16", 
         assert not bad.any(), (bad.mean(), np.argwhere(bad)[:3])
 
 
-ROWS = [  # Hq, Hkv, d, page, lens, news: few rows, several tiles of them
+ROWS = [  # Hq, Hkv, d, page, lens, news: few rows, several tiles of them, many
     (4, 1, 64, 16, [192], [1]), (4, 1, 128, 16, [190], [16]), (8, 2, 64, 32, [300, 100], [7, 5]),
-    (4, 1, 64, 16, [3000], [1]), (8, 2, 128, 16, [2500, 1900], [5, 1])]
+    (4, 1, 64, 16, [192], [192]), (4, 1, 128, 16, [187], [187]), (6, 2, 64, 16, [400, 130], [390, 130]),
+    (4, 1, 64, 16, [3000], [1]), (8, 2, 128, 16, [2500, 1900], [5, 1]), (4, 1, 128, 64, [700], [300])]
 GAPS = [5, 12, 13, 21, 22, 25, 31, 40, 90]
 
 
@@ -133,7 +143,8 @@ def test_small_weights_on_pages_of_large_scale(Hq, Hkv, d, page, lens, news, gap
 
 
 @pytest.mark.parametrize("Hq,Hkv,d,page,lens,news", [
-    (4, 1, 64, 16, [6500], [1]), (8, 1, 128, 16, [6500], [3])])     # shares of all tiles, joined afterwards
+    (4, 1, 64, 16, [6500], [1]), (8, 1, 128, 16, [6500], [3]),      # shares of all tiles, joined afterwards
+    (16, 8, 64, 64, [600, 600], [600, 600])])                       # as many tiles of rows as SMs: no runs to join
 @pytest.mark.parametrize("gap", [13, 40])
 def test_long_calls_with_pages_of_far_scales(Hq, Hkv, d, page, lens, news, gap):
     s, g = 118, 118 + gap
@@ -142,7 +153,7 @@ def test_long_calls_with_pages_of_far_scales(Hq, Hkv, d, page, lens, news, gap):
     _run(Hq, Hkv, d, page, lens, news, [121], [s, g, s], light=-gap * np.log(2.0), seed=3)
 
 
-@pytest.mark.parametrize("news", [[1], [16]])
+@pytest.mark.parametrize("news", [[1], [16], [180]])
 @pytest.mark.parametrize("small", [0, 1, 2])
 def test_the_smallest_scales(news, small):
     """Pages of zeros and of values near the smallest beside ordinary ones, and a cache of nothing else."""
@@ -153,7 +164,7 @@ def test_the_smallest_scales(news, small):
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp16"])
 def test_repeats_are_equal(dtype):
-    """The same call again gives the same bits, pages of far scales included."""
+    """The same call again gives the same bits, runs that are joined and pages of far scales included."""
     B, Hq, Hkv, d, page, lens = 2, 8, 2, 64, 16, [900, 700]
     cols = 57
     table = np.random.default_rng(0).permutation(B * cols).reshape(B, cols)
@@ -162,7 +173,7 @@ def test_repeats_are_equal(dtype):
     for far in (False, True):
         if far:
             cache.vs[::3] = 90
-        for cu in ([0, 1, 4]):
+        for cu in ([0, 200, 400], [0, 1, 4]):
             runs = []
             for _ in range(4):
                 w = torch.zeros((B, Hkv, cols * page), device="cuda")
