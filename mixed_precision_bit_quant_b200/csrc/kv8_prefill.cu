@@ -587,7 +587,8 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const AttnParams
 //
 // One CTA takes 128 tokens of a sequence and kv head and walks the tiles of 128 query rows
 // that see them: S^T = K Q^T puts a token on a TMEM lane, so a token's sum over rows
-// is a thread's sum over columns -- no exchange, and in a fixed order.
+// is a thread's sum over columns -- no exchange, and in a fixed order.  K's codes enter bare, and a
+// page's scale multiplies its tokens' logits: a thread's own factor.
 //   warps 0-3, 4-7  the even and the odd row tiles' exponentials and sums
 //   warp 8     brings the row tiles' FP16 images, which prefill_kernel left in the workspace,
 //              by bulk copies, and the rows' scales and log-sum-exps
@@ -635,60 +636,51 @@ __global__ void __launch_bounds__(kTwThreads, 2) tile_weights_kernel(const AttnP
   auto BAR = [&](int k) -> uint32_t { return sb + L::OFF_BAR + 8 * k; };
   volatile uint32_t* misc = reinterpret_cast<volatile uint32_t*>(smem + L::OFF_MISC);
   volatile int* abort = reinterpret_cast<volatile int*>(smem + L::OFF_MISC + 4);
-  int* eref = reinterpret_cast<int*>(smem + L::OFF_MISC + 8);
   if (tid == 0) {
     for (int k = 0; k < NTWBAR; ++k) mbar_init(BAR(k), k >= WEMPTY && k < WDRAIN ? 4 : 1);
     *abort = 0;
-    *eref = 0;
     fence_mbar_init();
   }
   if (warp == 9) {
     tmem_alloc(smem_u32(smem + L::OFF_MISC), 256);
     tmem_relinquish();
   }
-  __syncthreads();
   const int32_t* trow = p.table + (long long)b * p.table_cols;
-  // Some row sees the token.  The table's entries of pages that none sees may be stale numbers of
-  // the pool: neither their codes nor their scales are read.
-  auto seen = [&](int tok) { return tok < s.len && any_visible(p, tok, 1, s.pos0, s.len - 1); };
-  // K's codes as FP16, each page relative to the largest exponent of the tile's visible pages
-  constexpr int VR = D / 16, ITEMS = 128 * VR / 256;
-  uint4 u[ITEMS];
-  int ks[ITEMS];
+  // Whether some row sees a token whose page is of the pool, and the place of the page's head.
+  // The table's entries of pages that none sees may be stale numbers of the pool: neither their
+  // codes nor their scales are read.
+  auto place = [&](int tok, long long& ph) -> bool {
+    if (tok >= s.len || !any_visible(p, tok, 1, s.pos0, s.len - 1)) return false;
+    const int pg = __ldg(trow + (tok >> p.page_log2));
+    ph = (long long)pg * p.Hkv + hk;
+    return pg >= 0 && pg < p.num_pages;
+  };
+  bool held = false;  // this thread's token has a place
+  float kf = 0.0f;    // and its page this scale
   if (warp < 8) {
-    int top = 0;
+    // K's codes as FP16
+    constexpr int VR = D / 16, ITEMS = 128 * VR / 256;
+    uint4 u[ITEMS];
+    long long ph;
 #pragma unroll
     for (int i = 0; i < ITEMS; ++i) {
       const int it = tid + 256 * i, tok = t0 + it / VR;
       u[i] = make_uint4(0, 0, 0, 0);
-      ks[i] = 0;
-      if (seen(tok)) {
-        const int pg = __ldg(trow + (tok >> p.page_log2));
-        if (pg >= 0 && pg < p.num_pages) {
-          const long long ph = (long long)pg * p.Hkv + hk;
-          ks[i] = __ldg(p.ks + ph);
-          u[i] = __ldg(reinterpret_cast<const uint4*>(p.k + ((ph << p.page_log2) + (tok & ((1 << p.page_log2) - 1))) * D) + it % VR);
-        }
-      }
-      top = max(top, ks[i]);
+      if (place(tok, ph))
+        u[i] = __ldg(reinterpret_cast<const uint4*>(p.k + ((ph << p.page_log2) + (tok & ((1 << p.page_log2) - 1))) * D) + it % VR);
     }
-    top = __reduce_max_sync(0xffffffffu, top);
-    if (lane == 0) atomicMax(eref, top);
-  }
-  __syncthreads();
-  const int kref = *eref;
-  if (warp < 8) {
+    held = place(t0 + (tid & 127), ph);
+    if (held) kf = scale_value(__ldg(p.ks + ph));
 #pragma unroll
     for (int i = 0; i < ITEMS; ++i) {
       const int it = tid + 256 * i, r = it / VR, ch = 2 * (it % VR);
-      const __half2 f = __float2half2_rn(pow2f(max(-24, ks[i] - kref + kUp)));
       const uint32_t rowa = sb + L::OFF_K + (ch >> 3) * 16384 + r * 128;
       sts128(rowa + (((ch & 7) ^ (r & 7)) << 4),
-             make_uint4(hmul2_u32(e4m3x2_to_h2(u[i].x & 0xFFFFu), f), hmul2_u32(e4m3x2_to_h2(u[i].x >> 16), f),
-                        hmul2_u32(e4m3x2_to_h2(u[i].y & 0xFFFFu), f), hmul2_u32(e4m3x2_to_h2(u[i].y >> 16), f)));
+             make_uint4(e4m3x2_to_h2(u[i].x & 0xFFFFu), e4m3x2_to_h2(u[i].x >> 16),
+                        e4m3x2_to_h2(u[i].y & 0xFFFFu), e4m3x2_to_h2(u[i].y >> 16)));
       sts128(rowa + ((((ch & 7) + 1) ^ (r & 7)) << 4),
-             make_uint4(hmul2_u32(e4m3x2_to_h2(u[i].z & 0xFFFFu), f), hmul2_u32(e4m3x2_to_h2(u[i].z >> 16), f),
-                        hmul2_u32(e4m3x2_to_h2(u[i].w & 0xFFFFu), f), hmul2_u32(e4m3x2_to_h2(u[i].w >> 16), f)));
+             make_uint4(e4m3x2_to_h2(u[i].z & 0xFFFFu), e4m3x2_to_h2(u[i].z >> 16),
+                        e4m3x2_to_h2(u[i].w & 0xFFFFu), e4m3x2_to_h2(u[i].w >> 16)));
     }
     fence_proxy_async_smem();
   }
@@ -723,7 +715,6 @@ __global__ void __launch_bounds__(kTwThreads, 2) tile_weights_kernel(const AttnP
     tc_commit_el(el, BAR(WDRAIN));
     mbar_wait(BAR(WDRAIN), 0, &never, kPfWaitNs);
   } else if (warp == 8) {
-    const float kf = pow2f(max(-126, kref - 127 - kUp));
     const long long tile0 = (long long)bk * p.row_tiles * 2 + rt0;
     int issued = 0;
     float lse2[4], qs;
@@ -752,7 +743,7 @@ __global__ void __launch_bounds__(kTwThreads, 2) tile_weights_kernel(const AttnP
         lse2[i] = (rt0 + j) * 128 + 4 * lane + i >= rows || lse2[i] == -INFINITY ? -INFINITY : -lse2[i];
       float* rp = reinterpret_cast<float*>(smem + L::OFF_ROW + (j % kTwRowSlots) * L::ROW);
       reinterpret_cast<float4*>(rp)[lane] = make_float4(lse2[0], lse2[1], lse2[2], lse2[3]);
-      if (lane == 0) rp[128] = fmaxf(qs * kf, kTiny);
+      if (lane == 0) rp[128] = qs;
       __syncwarp();
       if (lane == 0) mbar_arrive(BAR(ROWS + j % kTwRowSlots));
       fetch(j + 1);
@@ -776,7 +767,7 @@ __global__ void __launch_bounds__(kTwThreads, 2) tile_weights_kernel(const AttnP
       }
       tc_fence_after();
       const float4* rp = reinterpret_cast<const float4*>(smem + L::OFF_ROW + (j % kTwRowSlots) * L::ROW);
-      const float sc = reinterpret_cast<const float*>(rp)[128];
+      const float sc = fmaxf(reinterpret_cast<const float*>(rp)[128] * kf, kTiny);
       const uint64_t sc2 = f2pack(sc, sc);
       const int r0 = (rt0 + j) * 128;
       const bool edge = !all_visible(p, t0, 128, s.pos0 + r0 / p.G, s.pos0 + (min(rows, r0 + 128) - 1) / p.G);
@@ -821,12 +812,9 @@ __global__ void __launch_bounds__(kTwThreads, 2) tile_weights_kernel(const AttnP
     tc_fence_after();
     tmem_dealloc(tmem, 256);
   }
-  if (tid < 128 && seen(t0 + tid)) {
-    const int pg = __ldg(trow + ((t0 + tid) >> p.page_log2));
-    if (pg >= 0 && pg < p.num_pages) {
-      float* w = p.w + (long long)bk * p.w_cols + t0 + tid;
-      *w += sum + reinterpret_cast<const float*>(smem + L::OFF_SUM)[tid];
-    }
+  if (tid < 128 && held) {
+    float* w = p.w + (long long)bk * p.w_cols + t0 + tid;
+    *w += sum + reinterpret_cast<const float*>(smem + L::OFF_SUM)[tid];
   }
 }
 

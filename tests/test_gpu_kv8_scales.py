@@ -93,13 +93,12 @@ def _run(Hq, Hkv, d, page, lens, news, ke, ve, window=0, sinks=0, dtype="bf16", 
     q = (1 + 0.01 * q if light else q).to(DT[dtype])
     if max(ke) > min(ke) + 12:
         q[..., 0] = 0
-    many = max(news) * (Hq // Hkv) > 64
-    weights = weights and not many
     w = torch.zeros((B, Hkv, cols * page), device="cuda") if weights else None
     o, lse = mq.kv8_attention(q.cuda(), cache, _i32(table), _i32(lens), cu=_i32(cu), max_q=max(news), window=window,
                               sinks=sinks, weights=w, want_lse=True)
     assert mq.device_status() == (0, 0)
     live = [x for x in ve if x > 0] or [0]
+    many = max(news) * (Hq // Hkv) > 64
     # (an exponent of -127 marks values below 2^-118, which count as zero beside pages of ordinary scale)
     ro, ob, rl, lb, rw, wb = _reference(pool, q.double().numpy(), table, lens, cu, window, sinks,
                                         many and max(live) - min(live) <= NEAR)
