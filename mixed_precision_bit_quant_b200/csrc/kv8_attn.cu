@@ -285,9 +285,10 @@ __global__ void __launch_bounds__(32 * kMergeWarps) merge_kernel(const AttnParam
 }
 
 // The weight sums of few rows: split_kernel left every visible logit (log2 domain, FP32), and
-// a thread adds up one token's rows with their final log-sum-exp.  Storing the logits costs
-// 8 bytes a row and token, a fraction of the token's 2 D bytes of codes (4 rows and D = 128:
-// 1/8); computing them again took as long as the attention itself (75 us of 142 at 32
+// a thread adds up one token's rows with their final log-sum-exp.  The logits lie in the order of
+// a row tile's span, so a window's take the window's room.  Storing them costs 8 bytes a row and
+// token: 1/8 of the token's 2 D bytes of codes for 4 rows and D = 128, and as much as the codes
+// for 32 rows; computing them again took as long as the attention itself (75 us of 142 at 32
 // sequences of up to 8191 tokens, against 8).  One thread adds a token's rows in order: the sum does
 // not depend on how the work was spread.
 constexpr int kWeightRows = 64;  // the most rows of split_kernel
@@ -301,8 +302,9 @@ __global__ void __launch_bounds__(kWeightThreads) logit_weights_kernel(const Att
   __shared__ int pos[kWeightRows];
   const int bk = blockIdx.y, b = bk / p.Hkv, hk = bk % p.Hkv;
   const Seq s = load_seq(p.lens, p.cu, b, p.n, p.max_q, p.max_len);
-  const int rows = s.nq * p.G, t0 = blockIdx.x * kWeightThreads * T + threadIdx.x;
-  if (blockIdx.x * kWeightThreads * T >= s.len || rows == 0) return;
+  const int rows = s.nq * p.G, t0 = blockIdx.x * kWeightThreads * T + (int)threadIdx.x;
+  const int tb = blockIdx.x * kWeightThreads * T;
+  if (tb >= s.len || rows == 0 || !any_visible(p, tb, kWeightThreads * T, max(s.pos0, 0), s.len - 1)) return;
   float* w = p.w + (long long)bk * p.w_cols;
   float sum[T], was[T];
 #pragma unroll
@@ -320,14 +322,17 @@ __global__ void __launch_bounds__(kWeightThreads) logit_weights_kernel(const Att
   __syncthreads();
   for (int r0 = 0; r0 < rows; r0 += R) {
     const float* at = p.logits + ((long long)bk * p.row_tiles + r0 / R) * p.logit_tokens * RW;
-    // a logit that its row does not see may be unwritten: it is loaded (without a branch, so
-    // that the loads go out together) and dropped
+    const Span<kTile> span = visible_span<kTile>(s.pos0 + r0 / p.G, s.pos0 + (min(rows, r0 + R) - 1) / p.G, p.window, p.sinks);
+    // a logit that its row does not see may be unwritten or have no place: one is loaded all the
+    // same (without a branch, so that the loads go out together) and dropped
     float2 x[T][RW / 2];
 #pragma unroll
-    for (int i = 0; i < T; ++i)
+    for (int i = 0; i < T; ++i) {
+      const int tok = t0 + i * kWeightThreads, v = span.index(tok / kTile);
+      const long long row = v < span.count ? (long long)v * kTile + tok % kTile : 0;
 #pragma unroll
-      for (int c = 0; c < RW / 2; ++c)
-        x[i][c] = *reinterpret_cast<const float2*>(at + (long long)min(t0 + i * kWeightThreads, s.len - 1) * RW + 2 * c);
+      for (int c = 0; c < RW / 2; ++c) x[i][c] = *reinterpret_cast<const float2*>(at + row * RW + 2 * c);
+    }
 #pragma unroll
     for (int c = 0; c < RW; ++c) {
       if (r0 + c >= rows) break;
@@ -396,7 +401,9 @@ static Plan make_plan(const thrift_kv8_shape& s, const thrift_kv8_mask& m, bool 
   p.slots_off = take(p.tiles128 || p.cluster ? 0 : (size_t)units * sizeof(int2));
   p.lse_off = take(with_w ? nrow * sizeof(float) : 0);
   p.logit_w = rows <= 2 ? 2 : rows <= 4 ? 4 : 8 * p.nt;
-  p.logit_tokens = (s.max_len + kTile - 1) / kTile * kTile;
+  // (a row tile's span has at most `tiles` tiles, and those of the longest sequence)
+  const long long whole = (s.max_len + kTile - 1) / kTile;
+  p.logit_tokens = (int)(tiles < whole ? tiles : whole) * kTile;
   // prefill_kernel's query tiles for tile_weights_kernel
   const size_t tiles128 = with_w && p.tiles128 ? (size_t)units * 2 : 0;
   p.image_off = take(tiles128 * 128 * s.d * 2);

@@ -20,7 +20,7 @@ struct AttnParams {
   float* part_o;
   int2* unit_slots;  // split_kernel: first slot and slots of a (sequence, kv head, row tile)
   float* lse2;      // [row] log2-domain log-sum-exp for the weights (or null)
-  float* logits;    // split_kernel's logits for the weight sums, [sequence, kv head, row tile][token][logit_w] (or null)
+  float* logits;    // split_kernel's logits for the weight sums, [sequence, kv head, row tile][token of the span][logit_w] (or null)
   uint8_t* q_image;  // prefill_kernel's query tiles and rows' scales for the weight sums (or null)
   float* q_scale;
   int logit_w, logit_tokens;
@@ -37,6 +37,10 @@ template <int T>
 struct Span {
   int s_tiles, a_tile, count;
   __device__ __forceinline__ int token(int v) const { return (v < s_tiles ? v : a_tile + (v - s_tiles)) * T; }
+  // the place of a sequence's tile: `count` or more for one past the end or between the two parts
+  __device__ __forceinline__ int index(int tile) const {
+    return tile < s_tiles ? tile : tile >= a_tile ? tile - a_tile + s_tiles : 0x7FFFFFFF;
+  }
 };
 template <int T>
 __device__ __forceinline__ Span<T> visible_span(int p_lo, int p_hi, int window, int sinks) {

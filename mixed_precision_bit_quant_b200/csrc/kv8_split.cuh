@@ -234,10 +234,10 @@ __device__ __forceinline__ void split_segment(const AttnParams& p, const Seq& s,
     }
   }
   auto step = [&](int it, Codes<D>& c, int pg, int ksc, int vsc) {
-    const int tok = span.token(v0 + warp + it * kSplitWarps);
+    const int v = v0 + warp + it * kSplitWarps, tok = span.token(v);
     if (pg < 0) {  // not visible: no weight
       if (p.logits != nullptr)
-        for (int i = lane; i < kTile * p.logit_w; i += 32) logit_row[(long long)tok * p.logit_w + i] = -INFINITY;
+        for (int i = lane; i < kTile * p.logit_w; i += 32) logit_row[(long long)v * kTile * p.logit_w + i] = -INFINITY;
       return;
     }
     float x[NT][4];
@@ -271,7 +271,7 @@ __device__ __forceinline__ void split_segment(const AttnParams& p, const Seq& s,
 #pragma unroll
       for (int n = 0; n < NT; ++n)
         if (8 * n + 2 * t < p.logit_w) {
-          float* at = logit_row + (long long)(tok + g) * p.logit_w + 8 * n + 2 * t;
+          float* at = logit_row + (long long)(v * kTile + g) * p.logit_w + 8 * n + 2 * t;
           *reinterpret_cast<float2*>(at) = make_float2(x[n][0], x[n][1]);
           *reinterpret_cast<float2*>(at + 8 * p.logit_w) = make_float2(x[n][2], x[n][3]);
         }

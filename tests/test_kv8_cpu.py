@@ -206,3 +206,20 @@ def test_a_call_follows_its_tensors_device(monkeypatch):
     assert seen == [(7, 100)]
     with pytest.raises(mq.ThriftError, match="THRIFT_ERR_INVALID"):
         _lib._kv8_call(lambda *a: 1, "x", torch.device("cuda", 0))
+
+
+def test_workspace_of_a_window_does_not_grow_with_the_text():
+    """The logits kept for the weight sums are the visible tokens', for every number of rows."""
+    f = mq.lib().thrift_kv8_attn_workspace_bytes
+    for max_q, Hq in ((1, 8), (1, 64), (4, 64), (8, 64), (40, 64)):
+        sizes = []
+        for n in (16384, 131072, 1 << 20):
+            s = _shape(B=8, Hq=Hq, Hkv=8, n=8 * max_q, max_q=max_q, max_len=n, table_cols=n // 64)
+            sizes.append(f(ctypes.byref(s), ctypes.byref(_lib.Kv8Mask(4096, 4, 0.0)), 1))
+            # without a window: a logit of every token, at least
+            if max_q * (Hq // 8) <= 64:
+                assert f(ctypes.byref(s), ctypes.byref(_lib.Kv8Mask(0, 0, 0.0)), 1) >= 4 * 8 * 8 * max_q * (Hq // 8) * n
+        assert sizes[0] == sizes[1] == sizes[2]
+        if max_q * (Hq // 8) <= 64:
+            rows = -(-max_q * (Hq // 8) // 16) * 16
+            assert sizes[0] <= 4 * 8 * 8 * rows * (4096 + 200) + (96 << 20)
