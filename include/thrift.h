@@ -339,7 +339,9 @@ THRIFT_API thrift_status thrift_decode_step(const thrift_decode_shape *shape, co
  * end may hold anything, NaN codes included.
  *
  * Limits: d in {64, 128}; page in {16, 32, 64, 128}; B * Hkv <= 65535;
- * table_cols * page <= 2^24 tokens a sequence; num_pages <= 2^30; n * Hq < 2^31.
+ * table_cols * page <= 2^24 tokens a sequence; num_pages <= 2^30; n * Hq < 2^31;
+ * R = max_q * Hq / Hkv <= 2^24, and where R <= 64 also
+ * B * Hkv * ceil(R / 8) * (ceil(max_len / 16) + 1) < 2^31.
  * Pool pointers 16-byte aligned, w 16, table, lens, cu, lse 4.
  * ------------------------------------------------------------------------ */
 enum { THRIFT_BF16 = 0, THRIFT_FP16 = 1 };
@@ -400,8 +402,11 @@ THRIFT_API thrift_status thrift_kv8_append(const thrift_kv8_shape *shape, const 
  * further apart those rows take the slower way of few rows (only values of pages
  * with e = -127, below 2^-118, then count as zero beside larger pages).  q must be
  * finite, logits below 2^21 in magnitude and values of V below 2^88.
- * ws: thrift_kv8_attn_workspace_bytes bytes (16-byte aligned; NULL if 0).  Calls
- * whose work can overlap on the GPU need their own.
+ * max_q picks the kernels of the whole call: up to 64 rows (max_q * Hq / Hkv) those
+ * of few rows.  A batch of single tokens with cu should have max_q 1.
+ * ws: thrift_kv8_attn_workspace_bytes bytes (16-byte aligned; NULL if 0); with w and
+ * up to 64 rows it holds an FP32 logit of every row and visible token.  Calls
+ * whose work can overlap on the GPU need their own.  No output may overlap an input.
  */
 typedef struct {
   int32_t window, sinks;  /* window 0: none (sinks is then without effect) */

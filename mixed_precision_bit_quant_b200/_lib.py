@@ -576,8 +576,9 @@ def kv8_attention(q: torch.Tensor, cache: Kv8Cache, table: torch.Tensor, lens: t
     """thrift_kv8_attn: attention of the new tokens' queries q [n, Hq, d] (bf16 or fp16, tokens may be strided)
     over the cache that already holds those tokens -> (o [n, Hq, d], lse fp32 [n, Hq] or None).  Causal; with
     window > 0 a query at position p sees t > p - window and the first `sinks` tokens.  table, lens, cu, max_q as
-    for kv8_append; max_len bounds lens (default: what the table holds).  weights: fp32 [B, Hkv, >= max_len], to
-    which each token's attention weights are added."""
+    for kv8_append, and max_q picks the kernel: a batch of single tokens that has a cu should pass 1.  max_len bounds
+    lens (default: what the table holds).  weights: fp32 [B, Hkv, >= max_len], to which each token's attention
+    weights are added."""
     _want_kv8(cache, "cache")
     qs = _kv8_tokens(q, "q", 0, cache.d, cache.device)
     n, Hq, d = q.shape

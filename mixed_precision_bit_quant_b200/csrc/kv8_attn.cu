@@ -131,7 +131,7 @@ __global__ void __launch_bounds__(kSplitThreads, resident_ctas(D, NT)) split_ker
 // A short unit (few tiles, and few units): one cluster of eight CTAs takes it, an eighth of its
 // tiles each, and joins the states through the cluster's shared memory -- no search for the
 // shares, no workspace, no second launch.  At one sequence of 517 tokens and 12 heads of 64
-// 5.3 us where split_kernel and merge_kernel take 6.5 + 3.1; at four windows of 4096 tokens 14.3
+// 5.3 us (kernels run over and over) where split_kernel and merge_kernel take 6.5 + 3.1; at four windows of 4096 tokens 14.3
 // where they take 15.7 + 3.6.
 constexpr int kCluster = 8;
 __device__ __forceinline__ uint32_t peer_address(uint32_t addr, uint32_t rank) {

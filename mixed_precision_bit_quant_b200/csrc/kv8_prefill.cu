@@ -15,12 +15,13 @@
 // for pages up to 2^21 smaller); the query enters as FP16 scaled by a power of two per row tile.
 // A run whose pages' scales lie further apart (K: 2^21; V: 2^12, beyond which small weights on
 // large pages would be lost in P's FP16) is walked as kv8_split.cuh does, where K and P carry each
-// page's scale for itself; only pages of exponent -127 (zeros, and values below 2^-118) may lie
-// further below the others, and count as zero then.
+// page's scale for itself (8.7 ms instead of 1.0 for the case below, every fifth page's V 2^21 smaller);
+// only pages of exponent -127 (zeros, and values below 2^-118) may lie further below the
+// others, and count as zero then.
 // 4096 queries over 16389 tokens (32 heads of 128, 4 a kv head): 987 us, 975 TFLOP/s, in repeated
 // calls (1015 us, 948 TFLOP/s, in turn with other work).  No pipe
-// bounds it: at 2048 queries over 4096 tokens the tensor cores work 42 % of the clocks in the mean
-// over the SMs (56 % on the busiest), the special-function unit 42 %, the ALUs 35 %.  A step's chain
+// bounds it: at 2048 queries over 4096 tokens the tensor cores work 40 % of the clocks in the mean
+// over the SMs (55 % on the busiest), the special-function unit 41 %, the ALUs 34 %.  A step's chain
 // of waits does -- S to registers, maximum, exponentials, P to tensor memory, two products -- of
 // which two row tiles keep two in flight; tensor memory holds no third.  Copies that skip work, at
 // 990 us with all of it: no exponentials 968, no conversion 1004, an eighth of Q K^T and a quarter of

@@ -152,8 +152,8 @@ __device__ __forceinline__ void split_sync() {
 // small scale is not lost beside pages that it does not see or hardly weighs (one e_r for the tile,
 // the largest e_v, did).  They are raised (and O rescaled) only when a logit, or a logit with its
 // page's scale, exceeds them by 4 binades: the common step needs one vote and no cross-lane maximum.
-//   Bound by HBM at 8 rows (8 sequences of 32768 tokens, 4 heads a group: 95 us, 5.6 TB/s); at 16
-// rows a step's own latencies bind (two passes of 16 rows over 8 x 16384 tokens: 74 us against 26
+//   Bound by HBM at 8 rows (8 sequences of 32768 tokens, 4 heads a group: 93 us, 5.8 TB/s); at 16
+// rows a step's own latencies bind (two passes of 16 rows over 8 x 16384 tokens: 79 us against 26
 // for the bytes; one pass of 32 rows with the codes in a shared-memory ring took 67, but the ring cost
 // the 8-row case 20 us).
 //   GROUP: one of several groups of kSplitThreads threads of a CTA (prefill_kernel's), with few

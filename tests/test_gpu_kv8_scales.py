@@ -182,3 +182,57 @@ def test_repeats_are_equal(dtype):
             assert mq.device_status() == (0, 0)
             for r in runs[1:]:
                 assert all(torch.equal(a, b) for a, b in zip(r, runs[0]))
+
+
+def test_a_captured_chunk_follows_the_scales_and_two_streams_do_not_meet():
+    """Whether scales lie far apart is decided when a call runs: one capture, replayed with other scales; and the
+    calls of two streams at once, each with its own workspace, as those alone."""
+    Hq, Hkv, d, page, L, n = 8, 2, 128, 16, 700, 150
+    cols = -(-L // page)
+    table = np.random.default_rng(0).permutation(cols)[None]
+    cache = _pool(cols, Hkv, page, d, 0, nan=False)
+    near = cache.vs.clone()
+    far = near.clone()
+    far[torch.from_numpy(table[0, 1::3]).cuda()] = 60
+    q = torch.randn((n, Hq, d), generator=torch.Generator().manual_seed(1)).to(torch.bfloat16).cuda()
+    t, ln, cu = _i32(table), _i32([L]), _i32([0, n])
+    size = mq.kv8_attention_workspace(q, cache, t, ln, cu=cu, weights=torch.zeros((1, Hkv, cols * page), device="cuda"))
+
+    def make():
+        return (torch.zeros((1, Hkv, cols * page), device="cuda"), torch.zeros_like(q), torch.zeros((n, Hq), device="cuda"),
+                torch.empty(size, dtype=torch.uint8, device="cuda"))
+
+    def call(w, o, lse, ws):
+        w.zero_()
+        mq.kv8_attention(q, cache, t, ln, cu=cu, weights=w, o=o, lse=lse, ws=ws)
+    alone = []
+    for s in (near, far):
+        cache.vs.copy_(s)
+        alone.append(make())
+        call(*alone[-1])
+    torch.cuda.synchronize()
+    assert not torch.equal(alone[0][1], alone[1][1])
+    streams, got = [torch.cuda.Stream() for _ in range(2)], [make(), make()]
+    for st, x in zip(streams, got):
+        with torch.cuda.stream(st):
+            call(*x)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call(*got[0])
+    for i in (0, 1, 0, 1):
+        cache.vs.copy_((near, far)[i])
+        torch.cuda.synchronize()
+        for x in got[0]:
+            x.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got[0][:3], alone[i][:3]))
+        for _ in range(5):
+            for st, x in zip(streams, got):
+                with torch.cuda.stream(st):
+                    call(*x)
+        torch.cuda.synchronize()
+        for x in got:
+            assert all(torch.equal(a, b) for a, b in zip(x[:3], alone[i][:3]))
+    assert mq.device_status() == (0, 0)
